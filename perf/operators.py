@@ -272,7 +272,8 @@ def run(state):
         tree = msa.MsaTree(s["parents"], s["n_nodes"])
         if s["op"] == "select":
             return msa.msa_tree_index_topk(dims, pages, tree, s["q_idx"], s["k_idx"], s["k_idx_pool"], want_margin=True)
-        return msa.msa_tree_sparse_attn(dims, pages, tree, s["q"], s["k"], s["v"], s["k_pool"], s["v_pool"], s["blocks"], want_lse=True)
+        return msa.msa_tree_sparse_attn(dims, pages, tree, s["q"], s["k"], s["v"], s["k_pool"], s["v_pool"], s["blocks"], want_lse=True,
+                                        out_dtype=torch.bfloat16)
     return {"rope": _rope, "append": _append, "copy": _copy, "select": _select, "attend": _attend}[s["op"]](s)
 
 
