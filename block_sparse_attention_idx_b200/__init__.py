@@ -7,7 +7,9 @@ Importing works without a GPU (the library loads without one); calling needs a C
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 
@@ -19,7 +21,8 @@ LIB_PATH = os.path.join(_PKG, "libmsa.so")
 MSA_OK, MSA_ERR_INVALID_ARG, MSA_ERR_UNSUPPORTED, MSA_ERR_WORKSPACE, MSA_ERR_CUDA, MSA_ERR_TIMEOUT, \
     MSA_ERR_DEVICE_CHECK = range(7)
 (MSA_OP_INDEX_TOPK, MSA_OP_INDEX_TOPK_LSE, MSA_OP_ATTN_FWD, MSA_OP_DECODE, MSA_OP_KL, MSA_OP_ATTN_BWD,
- MSA_OP_LSE_IDX_LOCAL, MSA_OP_KL_DENSE) = range(8)
+ MSA_OP_LSE_IDX_LOCAL, MSA_OP_KL_DENSE, MSA_OP_TREE_INDEX_TOPK, MSA_OP_TREE_ATTN) = range(10)
+MSA_BF16, MSA_F32 = range(2)
 
 
 class MsaError(RuntimeError):
@@ -36,6 +39,20 @@ class _Dims(ctypes.Structure):
 
 class _KeyRanges(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int32), ("tok0", ctypes.c_int32 * 2), ("ntok", ctypes.c_int32 * 2)]
+
+
+class _RopeSeg(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("inv_freq", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("dim", ctypes.c_int), ("rot", ctypes.c_int), ("amp", ctypes.c_float)]
+
+
+class _Pages(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("cache_len", ctypes.c_void_p), ("num_pages", ctypes.c_int)]
+
+
+class _Tree(ctypes.Structure):
+    _fields_ = [("parents", ctypes.c_void_p), ("n_nodes", ctypes.c_void_p), ("T", ctypes.c_int)]
 
 
 def _held(held, k_idx_local) -> _KeyRanges:
@@ -70,6 +87,22 @@ class MsaDims:
     def c(self) -> _Dims:
         return _Dims(self.B, self.N, self.H_q, self.H_kv, self.d, self.d_idx, self.block_k, self.topk,
                      self.scale, self.scale_idx)
+
+
+@dataclass
+class MsaPages:
+    """msa_pages: where each sequence's cached tokens lie. page_table int32 [B, ceil(N / block_k)] (page ids of
+    the pools, in position order) and cache_len int32 [B], on the device."""
+    page_table: torch.Tensor
+    cache_len: torch.Tensor
+
+
+@dataclass
+class MsaTree:
+    """msa_tree: T drafted tokens per sequence. parents int32 [B, T] (-1: follows the cache; else a lower
+    node number) and n_nodes int32 [B], on the device."""
+    parents: torch.Tensor
+    n_nodes: torch.Tensor
 
 
 _lib = None
@@ -111,6 +144,15 @@ def lib() -> ctypes.CDLL:
         L.msa_debug_wait_probe.restype = ctypes.c_int
         L.msa_debug_exp2_fma.argtypes = [P, P, ctypes.c_int64, P]
         L.msa_debug_exp2_fma.restype = ctypes.c_int
+        PG, TR, I64 = ctypes.POINTER(_Pages), ctypes.POINTER(_Tree), ctypes.c_int64
+        for fn in ("msa_rope_fwd", "msa_rope_bwd"):
+            getattr(L, fn).argtypes = [ctypes.POINTER(_RopeSeg), I, I64, P, I, I, I, P]
+        L.msa_cache_append.argtypes = [D, PG, I, P, P, P, I, P, P, P, P, P, P, S, P]
+        L.msa_cache_copy_pages.argtypes = [D, I, I, P, P, P, P, P, P, S, P]
+        L.msa_tree_workspace_size.argtypes = [I, D, I, ctypes.POINTER(ctypes.c_size_t)]
+        L.msa_tree_index_topk.argtypes = [D, PG, TR, P, P, P, P, P, P, S, P]
+        L.msa_tree_sparse_attn.argtypes = [D, PG, TR, P, P, P, P, P, P, P, P, P, S, P]
+        L.msa_tree_sparse_attn_bf16.argtypes = [D, PG, TR, P, P, P, P, P, P, P, P, P, S, P]
         L.msa_profile_enable.argtypes = [ctypes.c_int]
         L.msa_profile_enable.restype = None
         L.msa_profile_read.argtypes = [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_double),
@@ -123,7 +165,9 @@ def lib() -> ctypes.CDLL:
                    "msa_sparse_attn_decode",
                    "msa_sparse_attn_decode_fp8idx", "msa_quantize_e4m3_rows", "msa_kl_fwd_grad",
                    "msa_sparse_attn_bwd", "msa_index_topk_local", "msa_topk_merge", "msa_lse_idx_local",
-                   "msa_lse_combine", "msa_get_device_status", "msa_kl_dense_fwd_grad"):
+                   "msa_lse_combine", "msa_get_device_status", "msa_kl_dense_fwd_grad", "msa_rope_fwd",
+                   "msa_rope_bwd", "msa_cache_append", "msa_cache_copy_pages", "msa_tree_workspace_size",
+                   "msa_tree_index_topk", "msa_tree_sparse_attn", "msa_tree_sparse_attn_bf16"):
             getattr(L, fn).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -288,6 +332,277 @@ def msa_sparse_attn_decode_fp8idx(dims: MsaDims, cache_len, q, q_idx, k_cache, v
                                                _p(out), _p(blocks), _p(margin), _p(ws), ws.numel(),
                                                _stream(stream, q.device)))
     return (out, blocks, margin) if want_margin else (out, blocks)
+
+
+def _on(stream):
+    """Context in which new buffers belong to `stream` (the allocator reuses them in its order)."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def msa_rope_inv_freq(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                      orig_len: int = 0, device=None):
+    """Inverse frequencies fp64 [rot / 2] and the amplitude, as (inv_freq, amp), for msa_rope_fwd / _bwd.
+
+    base ** (-2 i / rot), and for contexts `factor` times longer than the trained one:
+      None      as is
+      "linear"  positions divided by factor (every frequency / factor)
+      "ntk"     base * factor ** (rot / (rot - 2)): the lowest frequency is divided by factor, the highest kept
+      "yarn"    frequencies that turn at least 32 times over orig_len tokens are kept, those that turn at most
+                once are divided by factor, a linear ramp over i between; amp = 0.1 ln(factor) + 1
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot must be even and at least 2, got {rot}")
+    if not (base > 1.0 and factor >= 1.0):
+        raise ValueError(f"base must exceed 1 and factor be at least 1, got {base} and {factor}")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', not {scaling!r}")
+    amp = 1.0
+    if scaling == "ntk" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** -(torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if orig_len < 1:
+            raise ValueError("yarn needs orig_len, the trained context length")
+
+        def pair(turns):  # the (fractional) pair that turns that often over orig_len
+            return rot * math.log(orig_len / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+        lo, hi = max(math.floor(pair(32)), 0), min(math.ceil(pair(1)), rot - 1)
+        ramp = ((torch.arange(rot // 2, dtype=torch.float64) - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        f = f / factor * ramp + f * (1 - ramp)
+        amp = 0.1 * math.log(factor) + 1
+    return f.to(device) if device is not None else f, amp
+
+
+def _token_rows(t: torch.Tensor, name: str):
+    """(tokens, heads, dim, elements between tokens) of a [..., heads, dim] tensor whose last two dims are
+    contiguous and whose leading dims have one stride (a column slice of a projection's output qualifies)."""
+    if t.dim() < 3:
+        raise ValueError(f"{name}: expected [..., heads, dim], got {tuple(t.shape)}")
+    heads, dim = t.shape[-2:]
+    if (dim > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != dim):
+        raise ValueError(f"{name}: heads and dim must be contiguous")
+    tokens, stride = 1, heads * dim
+    for size, st in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if size == 1:
+            continue
+        if tokens == 1:
+            stride = st
+        elif st != tokens * stride:
+            raise ValueError(f"{name}: the leading dimensions must have one stride")
+        tokens *= size
+    return tokens, heads, dim, stride
+
+
+def _rope(fn: str, xs, freqs, positions, interleaved, outs, out_dtype, stream):
+    xs, freqs = list(xs), list(freqs)
+    if not xs or len(freqs) != len(xs) or (outs is not None and len(outs) != len(xs)):
+        raise ValueError("need one (inv_freq, amp) pair, and with outs one output, per tensor")
+    dev, dtype = xs[0].device, xs[0].dtype
+    types = {torch.bfloat16: MSA_BF16, torch.float32: MSA_F32}
+    if outs is not None:
+        outs = list(outs)
+        if out_dtype not in (None, outs[0].dtype):
+            raise ValueError(f"outs are {outs[0].dtype}, out_dtype is {out_dtype}")
+        out_dtype = outs[0].dtype
+    out_dtype = dtype if out_dtype is None else out_dtype
+    if dtype not in types or out_dtype not in types:
+        raise ValueError(f"tensors must be torch.bfloat16 or torch.float32, got {dtype} -> {out_dtype}")
+    for i, x in enumerate(xs):
+        if x.device.type != "cuda":
+            raise ValueError(f"xs[{i}] must be a CUDA tensor (the library takes device pointers), got {x.device}")
+    if outs is None:
+        with _on(stream):
+            outs = [torch.empty(x.shape, dtype=out_dtype, device=dev) for x in xs]
+    seg = (_RopeSeg * len(xs))()
+    tokens = xs[0].numel() // max(1, xs[0].shape[-1] * xs[0].shape[-2]) if xs[0].dim() >= 3 else 0
+    for i, (x, y, (f, amp)) in enumerate(zip(xs, outs, freqs)):
+        for t, name, dt in ((x, f"xs[{i}]", dtype), (y, f"outs[{i}]", out_dtype)):
+            if t.device != dev or t.dtype != dt:
+                raise ValueError(f"{name}: expected {dt} on {dev}, got {t.dtype} on {t.device}")
+        if x.shape != y.shape:
+            raise ValueError(f"outs[{i}]: expected shape {tuple(x.shape)}, got {tuple(y.shape)}")
+        n, heads, dim, sx = _token_rows(x, f"xs[{i}]")
+        _, _, _, sy = _token_rows(y, f"outs[{i}]")
+        if (x.numel() // (heads * dim) if heads * dim else 0) != tokens:
+            raise ValueError(f"xs[{i}] has another number of tokens than xs[0]")
+        if f.dim() != 1:
+            raise ValueError("inv_freq must be fp64 [rot / 2]")
+        _need(f, "inv_freq", f.shape, torch.float64, dev)
+        seg[i] = _RopeSeg(x.data_ptr(), y.data_ptr(), sx, sy, f.data_ptr(), heads, dim, 2 * f.numel(), amp)
+    if positions is not None:
+        _need(positions, "positions", positions.shape, torch.int32, dev)
+        if positions.numel() != tokens:
+            raise ValueError(f"positions: expected {tokens} values, got {positions.numel()}")
+    st = _stream(stream, dev)
+    if tokens == 0:
+        return outs
+    _check(fn, getattr(lib(), fn)(seg, len(xs), tokens, _p(positions), int(interleaved), types[dtype],
+                                  types[out_dtype], st))
+    return outs
+
+
+def msa_rope_fwd(xs, freqs, positions=None, interleaved: bool = False, outs=None, out_dtype=None, stream=None):
+    """Rotary positions of up to 8 tensors [..., heads, dim] (Q, K, Q_idx, K_idx of a step) in one launch.
+    freqs: one (inv_freq fp64 [rot / 2], amp) per tensor, e.g. from msa_rope_inv_freq; positions int32 with one
+    value per token (None: the token's index). Returns outs (new, contiguous, of out_dtype or the inputs' type,
+    unless given; an input itself for in place)."""
+    return _rope("msa_rope_fwd", xs, freqs, positions, interleaved, outs, out_dtype, stream)
+
+
+def msa_rope_bwd(dys, freqs, positions=None, interleaved: bool = False, outs=None, out_dtype=None, stream=None):
+    """Gradient of msa_rope_fwd with respect to its tensors: the upstream gradients (fp32, as the attention and
+    KL gradients are, or bf16) through the transposed rotation."""
+    return _rope("msa_rope_bwd", dys, freqs, positions, interleaved, outs, out_dtype, stream)
+
+
+def _status_ws(ws, dev):
+    """The optional status workspace of the cache operations."""
+    if ws is not None and (ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != dev):
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
+    return _p(ws), 0 if ws is None else ws.numel()
+
+
+def _pools(dims: MsaDims, pools, names, dev) -> int:
+    """Checks the pools and returns their number of pages."""
+    n = pools[0].shape[0] if pools[0].dim() else 0
+    kv, idx = (n, dims.block_k, dims.H_kv, dims.d), (n, dims.block_k, dims.d_idx)
+    for t, name in zip(pools, names):
+        _need(t, name, idx if name.startswith("k_idx") else kv, torch.bfloat16, dev)
+    return n
+
+
+def _pages(dims: MsaDims, pages: MsaPages, num_pages: int, dev) -> _Pages:
+    _need(pages.page_table, "page_table", (dims.B, -(-dims.N // dims.block_k)), torch.int32, dev)
+    _need(pages.cache_len, "cache_len", (dims.B,), torch.int32, dev)
+    return _Pages(pages.page_table.data_ptr(), pages.cache_len.data_ptr(), num_pages)
+
+
+def msa_cache_append(dims: MsaDims, pages: MsaPages, k, v, k_idx, k_pool, v_pool, k_idx_pool, n_new, rows=None, ws=None,
+                     stream=None):
+    """Writes n_new[b] (int32 [B]) new tokens of each sequence behind its cache_len[b] cached ones: rows 0, 1, ...
+    of k, v bf16 [B,T,H_kv,d] and k_idx bf16 [B,T,d_idx], or with rows (int32 [B,T_new]) row rows[b,i] for the
+    i-th. cache_len is the caller's to advance. ws (256 bytes) receives the status word if given."""
+    dev = k.device
+    T = k.shape[1] if k.dim() == 4 else 0
+    _need(k, "k", (dims.B, T, dims.H_kv, dims.d), torch.bfloat16, dev)
+    _need(v, "v", (dims.B, T, dims.H_kv, dims.d), torch.bfloat16, dev)
+    _need(k_idx, "k_idx", (dims.B, T, dims.d_idx), torch.bfloat16, dev)
+    _need(n_new, "n_new", (dims.B,), torch.int32, dev)
+    T_new = T
+    if rows is not None:
+        T_new = rows.shape[1] if rows.dim() == 2 else 0
+        _need(rows, "rows", (dims.B, T_new), torch.int32, dev)
+    n = _pools(dims, (k_pool, v_pool, k_idx_pool), ("k_pool", "v_pool", "k_idx_pool"), dev)
+    pg = _pages(dims, pages, n, dev)
+    wp, wn = _status_ws(ws, dev)
+    _check("msa_cache_append",
+           lib().msa_cache_append(ctypes.byref(dims.c()), ctypes.byref(pg), T, _p(k), _p(v), _p(k_idx), T_new,
+                                  _p(n_new), _p(rows), _p(k_pool), _p(v_pool), _p(k_idx_pool), wp, wn,
+                                  _stream(stream, dev)))
+
+
+def msa_cache_copy_pages(dims: MsaDims, src, dst, k_pool, v_pool, k_idx_pool, ws=None, stream=None):
+    """Page dst[i] of the three pools becomes a copy of page src[i]. src and dst are int32 CUDA tensors [n], or
+    sequences of page numbers, which are then checked here: in range, dst distinct, and no page in both."""
+    dev = k_pool.device
+    n_pages = _pools(dims, (k_pool, v_pool, k_idx_pool), ("k_pool", "v_pool", "k_idx_pool"), dev)
+    if not torch.is_tensor(src) and not torch.is_tensor(dst):
+        src, dst = [int(p) for p in src], [int(p) for p in dst]
+        if len(src) != len(dst):
+            raise ValueError(f"src has {len(src)} pages, dst {len(dst)}")
+        if any(not 0 <= p < n_pages for p in src + dst):
+            raise ValueError(f"page numbers must be in [0, {n_pages})")
+        if len(set(dst)) != len(dst) or set(dst) & set(src):
+            raise ValueError("dst pages must be distinct and none of them a src page")
+        with _on(stream):
+            src = torch.tensor(src, dtype=torch.int32, device=dev)
+            dst = torch.tensor(dst, dtype=torch.int32, device=dev)
+    elif not (torch.is_tensor(src) and torch.is_tensor(dst)):
+        raise ValueError("src and dst must both be tensors or both sequences")
+    _need(src, "src", (src.numel(),), torch.int32, dev)
+    _need(dst, "dst", (src.numel(),), torch.int32, dev)
+    wp, wn = _status_ws(ws, dev)
+    st = _stream(stream, dev)
+    _check("msa_cache_copy_pages",
+           lib().msa_cache_copy_pages(ctypes.byref(dims.c()), n_pages, src.numel(), _p(src) if src.numel() else None,
+                                      _p(dst) if src.numel() else None, _p(k_pool), _p(v_pool), _p(k_idx_pool), wp, wn, st))
+
+
+def msa_tree_workspace_size(op: int, dims: MsaDims, T: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("msa_tree_workspace_size", lib().msa_tree_workspace_size(op, ctypes.byref(dims.c()), T, ctypes.byref(n)))
+    return n.value
+
+
+def tree_workspace(op: int, dims: MsaDims, T: int, device) -> torch.Tensor:
+    """A device workspace buffer of the size a tree operation needs (256-byte aligned by the allocator)."""
+    return torch.empty(max(msa_tree_workspace_size(op, dims, T), 256), dtype=torch.uint8, device=device)
+
+
+def _tree(dims: MsaDims, tree: MsaTree, dev):
+    T = tree.parents.shape[1] if tree.parents.dim() == 2 else 0
+    _need(tree.parents, "parents", (dims.B, T), torch.int32, dev)
+    _need(tree.n_nodes, "n_nodes", (dims.B,), torch.int32, dev)
+    return T, _Tree(tree.parents.data_ptr(), tree.n_nodes.data_ptr(), T)
+
+
+def _tree_ws(ws, op: int, dims: MsaDims, T: int, dev, stream) -> torch.Tensor:
+    if ws is None:
+        with _on(stream):
+            return tree_workspace(op, dims, T, dev)
+    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != dev:
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
+    return ws
+
+
+def msa_tree_index_topk(dims: MsaDims, pages: MsaPages, tree: MsaTree, q_idx, k_idx, k_idx_pool, want_margin=False, ws=None,
+                        stream=None):
+    """Block selection of drafted tokens over a paged cache: q_idx bf16 [B,T,H_kv,d_idx], the drafted k_idx bf16
+    [B,T,d_idx], the cache's k_idx_pool. dims.N is the page table's capacity. Returns blocks int32
+    [B,T,H_kv,topk+1]; with want_margin, also the cutoff margins fp32 [B,T,H_kv]."""
+    dev = q_idx.device
+    T, tr = _tree(dims, tree, dev)
+    _need(q_idx, "q_idx", (dims.B, T, dims.H_kv, dims.d_idx), torch.bfloat16, dev)
+    _need(k_idx, "k_idx", (dims.B, T, dims.d_idx), torch.bfloat16, dev)
+    pg = _pages(dims, pages, _pools(dims, (k_idx_pool,), ("k_idx_pool",), dev), dev)
+    ws = _tree_ws(ws, MSA_OP_TREE_INDEX_TOPK, dims, T, dev, stream)
+    with _on(stream):
+        blocks = torch.empty(dims.B, T, dims.H_kv, dims.topk + 1, dtype=torch.int32, device=dev)
+        margin = torch.empty(dims.B, T, dims.H_kv, dtype=torch.float32, device=dev) if want_margin else None
+    _check("msa_tree_index_topk",
+           lib().msa_tree_index_topk(ctypes.byref(dims.c()), ctypes.byref(pg), ctypes.byref(tr), _p(q_idx), _p(k_idx),
+                                     _p(k_idx_pool), _p(blocks), _p(margin), _p(ws), ws.numel(), _stream(stream, dev)))
+    return (blocks, margin) if want_margin else blocks
+
+
+def msa_tree_sparse_attn(dims: MsaDims, pages: MsaPages, tree: MsaTree, q, k, v, k_pool, v_pool, blocks, want_lse=False,
+                         out_dtype=torch.float32, out=None, ws=None, stream=None):
+    """Sparse attention of drafted tokens: q bf16 [B,T,H_q,d], the drafted k, v bf16 [B,T,H_kv,d], the cache's
+    pools, blocks from msa_tree_index_topk. Returns out [B,T,H_q,d] (fp32, or bf16 by
+    msa_tree_sparse_attn_bf16) and LSE fp32 [B,T,H_q] (or None). `out` may be given to be written in place."""
+    dev = q.device
+    T, tr = _tree(dims, tree, dev)
+    _need(q, "q", (dims.B, T, dims.H_q, dims.d), torch.bfloat16, dev)
+    _need(k, "k", (dims.B, T, dims.H_kv, dims.d), torch.bfloat16, dev)
+    _need(v, "v", (dims.B, T, dims.H_kv, dims.d), torch.bfloat16, dev)
+    _need(blocks, "blocks", (dims.B, T, dims.H_kv, dims.topk + 1), torch.int32, dev)
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out_dtype must be torch.float32 or torch.bfloat16, not {out_dtype}")
+    pg = _pages(dims, pages, _pools(dims, (k_pool, v_pool), ("k_pool", "v_pool"), dev), dev)
+    ws = _tree_ws(ws, MSA_OP_TREE_ATTN, dims, T, dev, stream)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+        lse = torch.empty(dims.B, T, dims.H_q, dtype=torch.float32, device=dev) if want_lse else None
+    _need(out, "out", tuple(q.shape), out_dtype, dev)
+    fn = "msa_tree_sparse_attn" if out_dtype == torch.float32 else "msa_tree_sparse_attn_bf16"
+    _check(fn, getattr(lib(), fn)(ctypes.byref(dims.c()), ctypes.byref(pg), ctypes.byref(tr), _p(q), _p(k), _p(v),
+                                  _p(k_pool), _p(v_pool), _p(blocks), _p(out), _p(lse), _p(ws), ws.numel(),
+                                  _stream(stream, dev)))
+    return out, lse
 
 
 def msa_sparse_attn_decode_noalloc(dims: MsaDims, cache_len, q, q_idx, k_cache, v_cache, k_idx_cache, out=None,
@@ -491,5 +806,7 @@ __all__ = ["MsaDims", "MsaError", "msa_workspace_size", "msa_index_topk", "msa_s
            "msa_quantize_e4m3_rows", "msa_kl_fwd_grad", "msa_sparse_attn_bwd", "msa_index_topk_local",
            "msa_topk_merge", "msa_lse_idx_local", "msa_lse_combine", "msa_get_device_status", "msa_status_string",
            "msa_version", "msa_profile_enable", "msa_profile_read", "msa_decode_noalloc_status",
-           "msa_debug_set_wait_ns", "msa_debug_wait_probe", "msa_debug_exp2_fma", "msa_kl_dense_fwd_grad", "workspace", "lib",
-           "LIB_PATH"]
+           "msa_debug_set_wait_ns", "msa_debug_wait_probe", "msa_debug_exp2_fma", "msa_kl_dense_fwd_grad", "MsaPages", "MsaTree",
+           "msa_rope_inv_freq", "msa_rope_fwd", "msa_rope_bwd", "msa_cache_append", "msa_cache_copy_pages",
+           "msa_tree_workspace_size", "msa_tree_index_topk", "msa_tree_sparse_attn", "tree_workspace", "workspace",
+           "lib", "LIB_PATH"]

@@ -18,6 +18,7 @@ constexpr size_t kStatusBytes = 256;
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int num_sms() {
     static int cache[64] = {0};
@@ -31,8 +32,8 @@ int num_sms() {
     return cache[dev];
 }
 
-// Sizes shared by every entry point.
-msa_status check_common(const msa_dims* d) {
+// Head layout, block size and sequence length limits shared by every entry point that takes msa_dims.
+msa_status check_sizes(const msa_dims* d) {
     if (!d) return MSA_ERR_INVALID_ARG;
     if (d->B < 1 || d->N < 1 || d->H_q < 1 || d->H_kv < 1 || d->topk < 1) return MSA_ERR_INVALID_ARG;
     if (d->H_q % d->H_kv != 0) return MSA_ERR_INVALID_ARG;
@@ -44,6 +45,13 @@ msa_status check_common(const msa_dims* d) {
     if (d->block_k != 32 && d->block_k != 64 && d->block_k != 128) return MSA_ERR_UNSUPPORTED;
     if (d->topk > 16) return MSA_ERR_UNSUPPORTED;
     if (d->N >= (1 << 24)) return MSA_ERR_UNSUPPORTED;
+    return MSA_OK;
+}
+
+// Sizes of the entry points that keep one list entry per (token, group, slot).
+msa_status check_common(const msa_dims* d) {
+    const msa_status s = check_sizes(d);
+    if (s != MSA_OK) return s;
     const double entries = (double)d->B * d->N * d->H_kv * (d->topk + 1);
     if (entries >= 2147483647.0 / 2) return MSA_ERR_UNSUPPORTED;
     return MSA_OK;
@@ -130,6 +138,119 @@ cudaError_t status_init(DevStatus* status, cudaStream_t st) {
     const unsigned long long w = g_wait_ns.load(std::memory_order_relaxed);
     if (e == cudaSuccess && w != 0) e = run_set_wait(status, w, st);
     return e;
+}
+
+// Paged caches: the pool's tokens are indexed with 31 bits, the page table has ceil(N / block_k) columns.
+int page_cols(const msa_dims* d) { return (d->N + d->block_k - 1) / d->block_k; }
+msa_status check_pool(const msa_dims* d, int num_pages) {
+    if (num_pages < 1) return MSA_ERR_INVALID_ARG;
+    return (long long)num_pages * d->block_k > 0x7fffffffLL ? MSA_ERR_UNSUPPORTED : MSA_OK;
+}
+msa_status check_pages(const msa_dims* d, const msa_pages* p) {
+    if (!p || !p->page_table || !p->cache_len || !aligned4(p->page_table) || !aligned4(p->cache_len))
+        return MSA_ERR_INVALID_ARG;
+    return check_pool(d, p->num_pages);
+}
+// An optional workspace that only carries the status word.
+msa_status status_only(void* ws, size_t ws_bytes, cudaStream_t st, DevStatus** status) {
+    *status = nullptr;
+    if (!ws) return MSA_OK;
+    const msa_status s = ws_check(ws, ws_bytes, kStatusBytes);
+    if (s != MSA_OK) return s;
+    *status = static_cast<DevStatus*>(ws);
+    return status_init(*status, st) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+}
+
+// Drafted-token trees: T <= 64 (ancestor sets are 64-bit words), at most 8192 blocks a sequence.
+msa_status check_tree_sizes(const msa_dims* d, int T) {
+    const msa_status s = check_sizes(d);
+    if (s != MSA_OK) return s;
+    if (T < 1) return MSA_ERR_INVALID_ARG;
+    if (T > kTreeMaxT || page_cols(d) > kTreeMaxBlocks) return MSA_ERR_UNSUPPORTED;
+    if ((double)d->B * T * d->H_q * d->d >= 2147483647.0 * 16) return MSA_ERR_UNSUPPORTED;
+    return (double)d->B * T * d->H_kv * (d->topk + 1) >= 2147483647.0 / 4 ? MSA_ERR_UNSUPPORTED : MSA_OK;
+}
+size_t ws_tree_index(const msa_dims* d, int T) {
+    return kStatusBytes + tree_index_ws_bytes(d->B, d->N, d->H_kv, d->block_k, T);
+}
+int tree_splits(const msa_dims* d, int T) {
+    return tree_attn_splits(d->B, T, d->H_q, d->H_kv, d->block_k, d->topk, num_sms());
+}
+size_t ws_tree_attn(const msa_dims* d, int T) {
+    return kStatusBytes + tree_attn_ws_bytes(d->B, T, d->H_q, d->d, tree_splits(d, T));
+}
+TreeArgs tree_args(const msa_dims* d, const msa_pages* p, const msa_tree* t, DevStatus* status) {
+    TreeArgs a{};
+    a.B = d->B; a.N = d->N; a.H_q = d->H_q; a.H_kv = d->H_kv; a.d = d->d; a.d_idx = d->d_idx;
+    a.block_k = d->block_k; a.topk = d->topk; a.T = t->T;
+    a.cols = page_cols(d);
+    a.num_pages = p->num_pages;
+    a.scale = eff_scale(d->scale, d->d);
+    a.scale_idx = eff_scale(d->scale_idx, d->d_idx);
+    a.page_table = p->page_table; a.cache_len = p->cache_len;
+    a.parents = t->parents; a.n_nodes = t->n_nodes;
+    a.status = status;
+    return a;
+}
+msa_status check_tree(const msa_dims* d, const msa_pages* p, const msa_tree* t) {
+    if (!d || !t) return MSA_ERR_INVALID_ARG;
+    msa_status s = check_tree_sizes(d, t->T);
+    if (s != MSA_OK) return s;
+    if (!t->parents || !t->n_nodes || !aligned4(t->parents) || !aligned4(t->n_nodes)) return MSA_ERR_INVALID_ARG;
+    return check_pages(d, p);
+}
+
+// A strided matrix of `rows` rows of `width` bytes, `pitch` bytes apart.
+struct Rect {
+    uintptr_t base;
+    int64_t rows, width, pitch;
+};
+// Whether two of them can share a byte. Exact where the pitches agree (column slices of one buffer), else
+// by their address ranges.
+bool overlap(const Rect& a, const Rect& b) {
+    if (a.rows == 0 || b.rows == 0) return false;
+    const uintptr_t ae = a.base + (a.rows - 1) * a.pitch + a.width, be = b.base + (b.rows - 1) * b.pitch + b.width;
+    if (ae <= b.base || be <= a.base) return false;
+    if (a.pitch != b.pitch || a.rows == 1 || b.rows == 1) return true;
+    const int64_t off = a.base <= b.base ? (int64_t)((b.base - a.base) % a.pitch)
+                                         : a.pitch - 1 - (int64_t)((a.base - b.base - 1) % a.pitch);
+    return off < a.width || off + b.width > a.pitch;
+}
+
+msa_status rope_call(const msa_rope_seg* seg, int nseg, int64_t tokens, const int32_t* positions, int interleaved,
+                     int x_type, int y_type, int back, msa_stream_t stream_) {
+    if (!seg || nseg < 1 || tokens < 0 || (positions && !aligned4(positions))) return MSA_ERR_INVALID_ARG;
+    if ((x_type != MSA_BF16 && x_type != MSA_F32) || (y_type != MSA_BF16 && y_type != MSA_F32)) return MSA_ERR_INVALID_ARG;
+    if (nseg > kRopeSegs || tokens >= (1LL << 31)) return MSA_ERR_UNSUPPORTED;
+    const int xs = x_type == MSA_F32 ? 4 : 2, ys = y_type == MSA_F32 ? 4 : 2;
+    RopeArgs a{};
+    Rect xr[kRopeSegs], yr[kRopeSegs];
+    for (int i = 0; i < nseg; ++i) {
+        const msa_rope_seg& g = seg[i];
+        if (!g.x || !g.y || !g.inv_freq || !aligned16(g.x) || !aligned16(g.y) || (reinterpret_cast<uintptr_t>(g.inv_freq) & 7u))
+            return MSA_ERR_INVALID_ARG;
+        if (g.heads < 1 || g.rot < 2 || g.rot % 2 != 0 || g.rot > g.dim || !isfinite(g.amp)) return MSA_ERR_INVALID_ARG;
+        if ((g.dim != 32 && g.dim != 64 && g.dim != 128) || g.heads > 4096) return MSA_ERR_UNSUPPORTED;
+        const int64_t row = (int64_t)g.heads * g.dim;
+        if (g.x_stride < row || g.y_stride < row || g.x_stride >= (1LL << 40) || g.y_stride >= (1LL << 40) ||
+            g.x_stride * xs % 16 != 0 || g.y_stride * ys % 16 != 0)
+            return MSA_ERR_INVALID_ARG;
+        xr[i] = {reinterpret_cast<uintptr_t>(g.x), tokens, row * xs, g.x_stride * xs};
+        yr[i] = {reinterpret_cast<uintptr_t>(g.y), tokens, row * ys, g.y_stride * ys};
+        if (overlap(xr[i], yr[i]) && (g.x != g.y || g.x_stride != g.y_stride || xs != ys)) return MSA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(yr[i], yr[j]) || overlap(yr[i], xr[j]) || overlap(xr[i], yr[j])) return MSA_ERR_INVALID_ARG;
+        RopeSeg& o = a.seg[i];
+        o.x = g.x; o.y = g.y; o.x_stride = g.x_stride; o.y_stride = g.y_stride; o.inv_freq = g.inv_freq;
+        o.heads = g.heads; o.dim = g.dim; o.rot = g.rot; o.amp = g.amp;
+        o.vec = 8;
+        while (g.rot / 2 % o.vec != 0) o.vec /= 2;
+    }
+    a.nseg = nseg;
+    a.tokens = tokens;
+    a.positions = positions;
+    a.back = back;
+    return cuda_status(run_rope(a, interleaved != 0, xs == 4, ys == 4, num_sms(), reinterpret_cast<cudaStream_t>(stream_)));
 }
 
 struct Carver {
@@ -447,6 +568,139 @@ msa_status msa_sparse_attn_bwd(const msa_dims* d, const void* q, const void* k, 
     e = run_csr_build(a.csr, blocks, d->B, d->N, d->H_kv, d->block_k, d->topk, 128 / G, status, st);
     if (e == cudaSuccess) e = run_attn_bwd(a, q, k, v, dout, out, num_sms(), st);
     return cuda_status(e);
+}
+
+msa_status msa_rope_fwd(const msa_rope_seg* seg, int nseg, int64_t tokens, const int32_t* positions, int interleaved,
+                        int x_type, int y_type, msa_stream_t stream) {
+    return rope_call(seg, nseg, tokens, positions, interleaved, x_type, y_type, 0, stream);
+}
+
+msa_status msa_rope_bwd(const msa_rope_seg* seg, int nseg, int64_t tokens, const int32_t* positions, int interleaved,
+                        int x_type, int y_type, msa_stream_t stream) {
+    return rope_call(seg, nseg, tokens, positions, interleaved, x_type, y_type, 1, stream);
+}
+
+msa_status msa_cache_append(const msa_dims* d, const msa_pages* p, int T, const void* k, const void* v,
+                            const void* k_idx, int T_new, const int32_t* n_new, const int32_t* rows, void* k_pool,
+                            void* v_pool, void* k_idx_pool, void* ws, size_t ws_bytes, msa_stream_t stream_) {
+    msa_status s = check_sizes(d);
+    if (s != MSA_OK) return s;
+    s = check_pages(d, p);
+    if (s != MSA_OK) return s;
+    if (T < 1 || T_new < 1 || (!rows && T_new > T)) return MSA_ERR_INVALID_ARG;
+    if (!k || !v || !k_idx || !n_new || !k_pool || !v_pool || !k_idx_pool || !aligned16(k) || !aligned16(v) ||
+        !aligned16(k_idx) || !aligned4(n_new) || (rows && !aligned4(rows)) || !aligned16(k_pool) ||
+        !aligned16(v_pool) || !aligned16(k_idx_pool))
+        return MSA_ERR_INVALID_ARG;
+    if ((long long)d->B * T_new >= (1LL << 31)) return MSA_ERR_UNSUPPORTED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_);
+    AppendArgs a{};
+    s = status_only(ws, ws_bytes, st, &a.status);
+    if (s != MSA_OK) return s;
+    a.B = d->B; a.N = d->N; a.T = T; a.T_new = T_new; a.cols = page_cols(d); a.num_pages = p->num_pages;
+    a.block_k = d->block_k;
+    a.page_table = p->page_table; a.cache_len = p->cache_len; a.n_new = n_new; a.rows = rows;
+    a.k = static_cast<const uint4*>(k); a.v = static_cast<const uint4*>(v); a.k_idx = static_cast<const uint4*>(k_idx);
+    a.k_pool = static_cast<uint4*>(k_pool); a.v_pool = static_cast<uint4*>(v_pool);
+    a.k_idx_pool = static_cast<uint4*>(k_idx_pool);
+    a.kv_vec = d->H_kv * d->d / 8; a.idx_vec = d->d_idx / 8;
+    return cuda_status(run_cache_append(a, st));
+}
+
+msa_status msa_cache_copy_pages(const msa_dims* d, int num_pages, int n, const int32_t* src, const int32_t* dst,
+                                void* k_pool, void* v_pool, void* k_idx_pool, void* ws, size_t ws_bytes,
+                                msa_stream_t stream_) {
+    msa_status s = check_sizes(d);
+    if (s != MSA_OK) return s;
+    s = check_pool(d, num_pages);
+    if (s != MSA_OK) return s;
+    if (n < 0 || (n > 0 && (!src || !dst || !aligned4(src) || !aligned4(dst))) || !k_pool || !v_pool || !k_idx_pool ||
+        !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_idx_pool))
+        return MSA_ERR_INVALID_ARG;
+    if (n > (1 << 22)) return MSA_ERR_UNSUPPORTED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_);
+    CopyArgs a{};
+    s = status_only(ws, ws_bytes, st, &a.status);
+    if (s != MSA_OK) return s;
+    a.src = src; a.dst = dst; a.num_pages = num_pages;
+    a.k_pool = static_cast<uint4*>(k_pool); a.v_pool = static_cast<uint4*>(v_pool);
+    a.k_idx_pool = static_cast<uint4*>(k_idx_pool);
+    a.kv_vec = (int64_t)d->block_k * d->H_kv * d->d / 8; a.idx_vec = (int64_t)d->block_k * d->d_idx / 8;
+    return cuda_status(run_cache_copy_pages(a, n, st));
+}
+
+msa_status msa_tree_workspace_size(int op, const msa_dims* d, int T, size_t* bytes) {
+    if (!bytes) return MSA_ERR_INVALID_ARG;
+    const msa_status s = check_tree_sizes(d, T);
+    if (s != MSA_OK) return s;
+    switch (op) {
+        case MSA_OP_TREE_INDEX_TOPK: *bytes = ws_tree_index(d, T); return MSA_OK;
+        case MSA_OP_TREE_ATTN: *bytes = ws_tree_attn(d, T); return MSA_OK;
+    }
+    return MSA_ERR_INVALID_ARG;
+}
+
+msa_status msa_tree_index_topk(const msa_dims* d, const msa_pages* p, const msa_tree* t, const void* q_idx,
+                               const void* k_idx, const void* k_idx_pool, int32_t* blocks, float* margin_out, void* ws,
+                               size_t ws_bytes, msa_stream_t stream_) {
+    msa_status s = check_tree(d, p, t);
+    if (s != MSA_OK) return s;
+    if (!q_idx || !k_idx || !k_idx_pool || !blocks || !aligned16(q_idx) || !aligned16(k_idx) || !aligned16(k_idx_pool) ||
+        !aligned16(blocks) || (margin_out && !aligned16(margin_out)))
+        return MSA_ERR_INVALID_ARG;
+    s = ws_check(ws, ws_bytes, ws_tree_index(d, t->T));
+    if (s != MSA_OK) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_);
+    DevStatus* status = static_cast<DevStatus*>(ws);
+    if (status_init(status, st) != cudaSuccess) return MSA_ERR_CUDA;
+    TreeArgs a = tree_args(d, p, t, status);
+    tree_index_carve(&a, static_cast<uint8_t*>(ws) + kStatusBytes);
+    a.blocks_out = blocks;
+    a.margin_out = margin_out;
+    return cuda_status(run_tree_index(a, q_idx, k_idx, k_idx_pool, num_sms(), st));
+}
+
+static msa_status tree_attn(const msa_dims* d, const msa_pages* p, const msa_tree* t, const void* q, const void* k,
+                            const void* v, const void* k_pool, const void* v_pool, const int32_t* blocks, float* out,
+                            __nv_bfloat16* out_bf16, float* lse, void* ws, size_t ws_bytes, msa_stream_t stream_) {
+    msa_status s = check_tree(d, p, t);
+    if (s != MSA_OK) return s;
+    const void* o = out ? static_cast<const void*>(out) : out_bf16;
+    if (!q || !k || !v || !k_pool || !v_pool || !blocks || !o || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+        !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(blocks) || !aligned16(o) || (lse && !aligned16(lse)))
+        return MSA_ERR_INVALID_ARG;
+    s = ws_check(ws, ws_bytes, ws_tree_attn(d, t->T));
+    if (s != MSA_OK) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_);
+    DevStatus* status = static_cast<DevStatus*>(ws);
+    if (status_init(status, st) != cudaSuccess) return MSA_ERR_CUDA;
+    TreeArgs a = tree_args(d, p, t, status);
+    a.blocks = blocks;
+    a.splits = tree_splits(d, t->T);
+    if (a.splits > 1) {
+        Carver cv{static_cast<uint8_t*>(ws) + kStatusBytes};
+        const size_t rows = (size_t)a.splits * d->B * t->T * d->H_q;
+        a.lse_part = reinterpret_cast<float*>(cv.take(rows * 4));
+        a.o_part = reinterpret_cast<float*>(cv.take(rows * d->d * 4));
+    }
+    a.out = out;
+    a.out_bf16 = out_bf16;
+    a.lse = lse;
+    return cuda_status(run_tree_attn(a, q, k, v, k_pool, v_pool, st));
+}
+
+msa_status msa_tree_sparse_attn(const msa_dims* d, const msa_pages* p, const msa_tree* t, const void* q, const void* k,
+                                const void* v, const void* k_pool, const void* v_pool, const int32_t* blocks, float* out,
+                                float* lse, void* ws, size_t ws_bytes, msa_stream_t stream) {
+    return tree_attn(d, p, t, q, k, v, k_pool, v_pool, blocks, out, nullptr, lse, ws, ws_bytes, stream);
+}
+
+msa_status msa_tree_sparse_attn_bf16(const msa_dims* d, const msa_pages* p, const msa_tree* t, const void* q,
+                                     const void* k, const void* v, const void* k_pool, const void* v_pool,
+                                     const int32_t* blocks, void* out, float* lse, void* ws, size_t ws_bytes,
+                                     msa_stream_t stream) {
+    return tree_attn(d, p, t, q, k, v, k_pool, v_pool, blocks, nullptr, static_cast<__nv_bfloat16*>(out), lse, ws,
+                     ws_bytes, stream);
 }
 
 msa_status msa_kl_fwd_grad(const msa_dims* d, const void* q, const void* k, const void* q_idx, const void* k_idx,

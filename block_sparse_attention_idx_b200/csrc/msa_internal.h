@@ -181,6 +181,81 @@ cudaError_t run_quantize_e4m3_rows(const void* x, int64_t rows, int n, uint8_t* 
 cudaError_t run_decode(const DecodeArgs& a, const void* q, const void* q_idx, const void* k_cache, const void* v_cache,
                        const void* k_idx_cache, void* out, int num_sms, cudaStream_t st);
 
+// ---------------------------------------------------------------- rotary positions (msa_rope.cu)
+constexpr int kRopeSegs = 8;
+struct RopeSeg {
+    const void* x;           // [tokens][heads][dim], heads x dim contiguous, x_stride elements between tokens
+    void* y;
+    int64_t x_stride, y_stride;
+    const double* inv_freq;  // [rot / 2]
+    int heads, dim, rot;
+    float amp;
+    int vec;                 // pairs per lane: the largest of 8, 4, 2, 1 that divides rot / 2
+    int heads_per_unit;      // set by run_rope
+};
+struct RopeArgs {
+    RopeSeg seg[kRopeSegs];
+    int nseg;
+    int64_t tokens;
+    const int32_t* positions;  // [tokens], or null: position = token
+    int back;                  // rotate by -angle
+    int units;                 // warps per token, set by run_rope
+    int unit0[kRopeSegs];      // first of a segment's units
+};
+cudaError_t run_rope(RopeArgs a, bool interleaved, bool x32, bool y32, int num_sms, cudaStream_t st);
+
+// ---------------------------------------------------------------- paged caches (msa_pages.cu)
+struct AppendArgs {
+    int B, N, T, T_new, cols, num_pages, block_k;
+    const int32_t *page_table, *cache_len, *n_new, *rows;  // rows [B, T_new] or null
+    const uint4 *k, *v, *k_idx;          // [B, T] tokens
+    uint4 *k_pool, *v_pool, *k_idx_pool;
+    int kv_vec, idx_vec;                 // 16-byte vectors of a token's K (or V) and of its K_idx
+    DevStatus* status;                   // or null
+};
+cudaError_t run_cache_append(const AppendArgs& a, cudaStream_t st);
+struct CopyArgs {
+    const int32_t *src, *dst;
+    int num_pages;
+    uint4 *k_pool, *v_pool, *k_idx_pool;
+    int64_t kv_vec, idx_vec;             // 16-byte vectors of a page
+    int kv_pieces, idx_pieces;           // set by run_cache_copy_pages
+    DevStatus* status;                   // or null
+};
+cudaError_t run_cache_copy_pages(CopyArgs a, int n, cudaStream_t st);
+
+// ---------------------------------------------------------------- drafted-token trees (msa_tree.cu, msa_tree_attn.cu)
+constexpr int kTreeMaxT = 64;       // drafted tokens of a sequence: a node's ancestors are one 64-bit set
+constexpr int kTreeMaxBlocks = 8192;
+struct TreeArgs {
+    int B, N, H_q, H_kv, d, d_idx, block_k, topk, T;
+    int cols;                        // columns of the page table: ceil(N / block_k)
+    int num_pages;
+    float scale, scale_idx;
+    const int32_t *page_table, *cache_len, *parents, *n_nodes;
+    unsigned long long* anc;         // [B, T] ancestor sets (selection workspace)
+    float* bmax;                     // [B, T * H_kv, bmax_ld] block maxima over the cache (selection workspace)
+    int bmax_ld;
+    int32_t* blocks_out;             // [B, T, H_kv, topk+1]
+    float* margin_out;               // [B, T, H_kv] or null
+    const int32_t* blocks;
+    int splits;                      // key splits of the attention
+    float* o_part;                   // [splits, B, T, H_q, d] normalised partial outputs (splits > 1)
+    float* lse_part;                 // [splits, B, T, H_q]
+    float* out;                      // [B, T, H_q, d], or null when out_bf16 is set
+    __nv_bfloat16* out_bf16;
+    float* lse;                      // [B, T, H_q] or null
+    DevStatus* status;
+};
+size_t tree_index_ws_bytes(int B, int N, int H_kv, int block_k, int T);
+void tree_index_carve(TreeArgs* a, void* base);
+cudaError_t run_tree_index(const TreeArgs& a, const void* q_idx, const void* k_idx, const void* k_idx_pool, int num_sms,
+                           cudaStream_t st);
+int tree_attn_splits(int B, int T, int H_q, int H_kv, int block_k, int topk, int num_sms);
+size_t tree_attn_ws_bytes(int B, int T, int H_q, int d, int splits);
+cudaError_t run_tree_attn(const TreeArgs& a, const void* q, const void* k, const void* v, const void* k_pool,
+                          const void* v_pool, cudaStream_t st);
+
 // ---------------------------------------------------------------- dense warm-up (msa_dense.cu)
 struct DenseLseArgs {
     int B, N, H_q, H_kv, G, d, block_k;

@@ -14,6 +14,8 @@
  * ---------------------------------------
  * - All tensor arguments are DEVICE pointers to dense, contiguous, row-major arrays, 16-byte
  *   aligned. "bf16" means IEEE bfloat16 stored as 2 bytes.
+ * - The int32 index arrays of the rotary, paged-cache and tree entries (positions, page tables, lengths,
+ *   counts, rows, page lists, parents) need 4-byte alignment only.
  * - The caller owns every buffer, the workspace and the stream. The library never allocates,
  *   frees or synchronises (except msa_get_device_status, which synchronises the given stream).
  *   Every call only enqueues work on `stream` and returns.
@@ -85,7 +87,9 @@ enum {
     MSA_OP_KL = 4,
     MSA_OP_ATTN_BWD = 5,
     MSA_OP_LSE_IDX_LOCAL = 6,
-    MSA_OP_KL_DENSE = 7
+    MSA_OP_KL_DENSE = 7,
+    MSA_OP_TREE_INDEX_TOPK = 8, /* msa_tree_workspace_size */
+    MSA_OP_TREE_ATTN = 9        /* msa_tree_workspace_size */
 };
 
 /*
@@ -310,6 +314,137 @@ MSA_API msa_status msa_kl_dense_fwd_grad(const msa_dims *dims, const void *q, co
                                          const void *k_idx, float grad_scale, float *loss, float *dq_idx,
                                          float *dk_idx, float *lse_out, void *ws, size_t ws_bytes,
                                          msa_stream_t stream);
+
+/*
+ * Rotary positions (no counterpart in the pages, whose inputs arrive rotated). A token's head of `dim`
+ * elements has its first `rot` rotated in pairs (a, b) by the angle position * inv_freq[i], i < rot / 2, and
+ * scaled by amp; the other dim - rot are copied:
+ *   y_a = amp (x_a cos - x_b sin),   y_b = amp (x_a sin + x_b cos)
+ * with (a, b) = (i, i + rot/2), or (2i, 2i+1) with `interleaved`. msa_rope_fwd applies it, msa_rope_bwd its
+ * transpose (-sin in place of sin): the gradient dx of an upstream dy (passed as x, written to y), and for
+ * amp = 1 the inverse rotation. One call rotates up to 8 tensors (Q, K, Q_idx and K_idx of a step) in one
+ * launch. Angles are reduced to a fraction of a turn in 64 bits, so that far positions keep their accuracy;
+ * cos and sin are fp32 (absolute error below 3e-7), the rotation is fp32, rounded once to y's type.
+ *   seg        host array of nseg tensors (read during the call), 1 <= nseg <= 8
+ *     x, y       [tokens, heads, dim] of x_type / y_type; the heads x dim elements of a token contiguous,
+ *                tokens x_stride / y_stride elements apart (a multiple of 16 bytes, at least heads * dim).
+ *                y may be x itself (same stride and type: in place); any other overlap of an output with an
+ *                input or another output gives MSA_ERR_INVALID_ARG (strided tensors of different strides
+ *                count as overlapping where their address ranges do)
+ *     inv_freq   fp64 [rot / 2] device, |inv_freq| below 2^31
+ *     heads      1 .. 4096;  dim in {32, 64, 128};  rot even, 2 .. dim;  amp finite
+ *   tokens     0 .. 2^31 - 1 (0 enqueues nothing)
+ *   positions  int32 [tokens] device, any sign; NULL: token t has position t
+ *   x_type, y_type  MSA_BF16 or MSA_F32
+ * A rot / 2 that is a multiple of 8 takes 16-byte accesses; others work, with narrower ones.
+ */
+enum { MSA_BF16 = 0, MSA_F32 = 1 };
+typedef struct msa_rope_seg {
+    const void *x;
+    void *y;
+    int64_t x_stride, y_stride;
+    const double *inv_freq;
+    int heads, dim, rot;
+    float amp;
+} msa_rope_seg;
+MSA_API msa_status msa_rope_fwd(const msa_rope_seg *seg, int nseg, int64_t tokens, const int32_t *positions,
+                                int interleaved, int x_type, int y_type, msa_stream_t stream);
+MSA_API msa_status msa_rope_bwd(const msa_rope_seg *seg, int nseg, int64_t tokens, const int32_t *positions,
+                                int interleaved, int x_type, int y_type, msa_stream_t stream);
+
+/*
+ * Paged caches (no counterpart in the pages). A page holds one KV block: pools k_pool, v_pool bf16
+ * [num_pages, block_k, H_kv, d] and k_idx_pool bf16 [num_pages, block_k, d_idx]. Token position p of sequence
+ * b is row p % block_k of page page_table[b, p / block_k]; sequence b holds cache_len[b] tokens, and dims->N is
+ * the capacity that the page table describes (ceil(N / block_k) columns; columns at or past a sequence's
+ * last page are not read). Sequences may share pages (a fork shares all of them); a page must belong to
+ * one sequence before tokens are appended to it. num_pages * block_k < 2^31.
+ */
+typedef struct msa_pages {
+    const int32_t *page_table; /* device [B, ceil(N / block_k)] */
+    const int32_t *cache_len;  /* device [B], 0 <= cache_len[b] <= N */
+    int num_pages;
+} msa_pages;
+
+/*
+ * msa_cache_append: token cache_len[b] + i of sequence b, i < n_new[b], is written into its page from row
+ *   rows[b, i] (or row i where rows is NULL) of the sequence's new tokens. cache_len is not changed (the caller
+ *   adds n_new). `rows` writes the accepted path of a drafted tree: its node numbers.
+ *   k, v bf16 [B, T, H_kv, d]; k_idx bf16 [B, T, d_idx]; n_new int32 [B] device, 0 <= n_new[b] <= T_new;
+ *   rows int32 [B, T_new] device or NULL (then T_new <= T), 0 <= rows[b, i] < T for i < n_new[b]
+ *   The pages that two written tokens share must be distinct pages of distinct sequences, as above; the
+ *   rest of the pools is left as it was. A token whose length, slot, page id or row is out of range
+ *   is not written.
+ * msa_cache_copy_pages: page dst[i] of the three pools becomes a copy of page src[i], i < n <= 2^22 (a forked
+ *   sequence's partly filled page before it is appended to; the moves that compact a pool). src, dst int32
+ *   [n] device. The dst pages must be distinct, and no page both copied from and to (src[i] == dst[i] excepted:
+ *   nothing is done): otherwise the pages concerned end with a mixture. A pair with an id out of range is
+ *   skipped.
+ * ws is optional for both: a 256-byte, 256-byte-aligned workspace that receives the status word
+ * (MSA_ERR_DEVICE_CHECK if anything was out of range), or NULL with ws_bytes 0 for no report and one launch
+ * less.
+ */
+MSA_API msa_status msa_cache_append(const msa_dims *dims, const msa_pages *pages, int T, const void *k, const void *v,
+                                    const void *k_idx, int T_new, const int32_t *n_new, const int32_t *rows,
+                                    void *k_pool, void *v_pool, void *k_idx_pool, void *ws, size_t ws_bytes,
+                                    msa_stream_t stream);
+MSA_API msa_status msa_cache_copy_pages(const msa_dims *dims, int num_pages, int n, const int32_t *src,
+                                        const int32_t *dst, void *k_pool, void *v_pool, void *k_idx_pool, void *ws,
+                                        size_t ws_bytes, msa_stream_t stream);
+
+/*
+ * Drafted-token trees over a paged cache (speculative decoding; with T = 1, one paged decode step). T tokens
+ * are drafted for each sequence; node n < n_nodes[b] continues node parents[b, n] < n, or the cache itself
+ * where that is -1. Node n with e drafted ancestors sits at position cache_len[b] + e and sees its virtual
+ * sequence: the cached tokens, its ancestors and itself, at positions cache_len[b] .. cache_len[b] + e. Its
+ * selection and attention are those of msa_sparse_attn_decode on a cache that holds that sequence. The
+ * drafted tokens' K, V and K_idx are dense inputs; msa_cache_append writes the accepted ones afterwards.
+ *   T        1 .. 64
+ *   parents  int32 [B, T] device, -1 <= parents[b, n] < n for n < n_nodes[b]
+ *   n_nodes  int32 [B] device, 0 <= n_nodes[b] <= T; rows of the other nodes get blocks -1, margin +inf,
+ *            output 0 and LSE -inf
+ * Needs ceil(N / block_k) <= 8192. Out-of-range values are reported as MSA_ERR_DEVICE_CHECK and read as: a
+ * length or count clamped into its range, a parent as -1, a page id as page 0, a block id as -1.
+ */
+typedef struct msa_tree {
+    const int32_t *parents;
+    const int32_t *n_nodes;
+    int T;
+} msa_tree;
+/* Workspace bytes of MSA_OP_TREE_INDEX_TOPK or MSA_OP_TREE_ATTN (on the current device). */
+MSA_API msa_status msa_tree_workspace_size(int op, const msa_dims *dims, int T, size_t *bytes);
+
+/*
+ * Block selection of every node: Top-k of its past blocks c < b_n by (block maximum desc, id asc) over the
+ * virtual sequence, plus the local block b_n = (cache_len[b] + e) / block_k; ascending, -1 padded.
+ *   q_idx bf16 [B, T, H_kv, d_idx]; k_idx bf16 [B, T, d_idx] (drafted); k_idx_pool the cache's
+ *   blocks int32 [B, T, H_kv, topk+1]                                                         (output)
+ *   margin_out fp32 [B, T, H_kv] or NULL: the cutoff margin of msa_sparse_attn_decode         (output)
+ */
+MSA_API msa_status msa_tree_index_topk(const msa_dims *dims, const msa_pages *pages, const msa_tree *tree,
+                                       const void *q_idx, const void *k_idx, const void *k_idx_pool, int32_t *blocks,
+                                       float *margin_out, void *ws, size_t ws_bytes, msa_stream_t stream);
+
+/*
+ * Sparse attention of every node over the tokens of its virtual sequence in its selected blocks.
+ *   q bf16 [B, T, H_q, d]; k, v bf16 [B, T, H_kv, d] (drafted); k_pool, v_pool the cache's
+ *   blocks int32 [B, T, H_kv, topk+1]: ids in [0, b_n], -1 entries ignored, an id given twice counts once;
+ *          normally msa_tree_index_topk's output. Without the local block the node does not see itself.
+ *   out    fp32 [B, T, H_q, d], or bf16 (the same result, rounded to nearest even) for the _bf16 entry (output)
+ *   lse    fp32 [B, T, H_q] or NULL: natural-log sum-exp of the scaled logits                     (output)
+ * A row that sees no token has output 0 and LSE -inf. Entries of V (of the drafted tokens of existing nodes and
+ * of the cached tokens below cache_len) must be finite: nodes share a block's product, so an infinity or NaN
+ * there may reach nodes that did not select it. What lies behind the last token, in pages or in
+ * the drafted arrays, may be anything.
+ */
+MSA_API msa_status msa_tree_sparse_attn(const msa_dims *dims, const msa_pages *pages, const msa_tree *tree,
+                                        const void *q, const void *k, const void *v, const void *k_pool,
+                                        const void *v_pool, const int32_t *blocks, float *out, float *lse, void *ws,
+                                        size_t ws_bytes, msa_stream_t stream);
+MSA_API msa_status msa_tree_sparse_attn_bf16(const msa_dims *dims, const msa_pages *pages, const msa_tree *tree,
+                                             const void *q, const void *k, const void *v, const void *k_pool,
+                                             const void *v_pool, const int32_t *blocks, void *out, float *lse,
+                                             void *ws, size_t ws_bytes, msa_stream_t stream);
 
 /*
  * Allocation-free decode step (no counterpart in the pages; a convenience of this library).
