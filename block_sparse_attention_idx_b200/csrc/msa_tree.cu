@@ -21,28 +21,31 @@ namespace {
 
 // -------------------------------------------------------------------------------------- index scan
 // Persistent CTAs (one per SM, a second grid dimension for every further 256 rows) take equal contiguous
-// ranges of all sequences' 128-token tiles. S = Q_idx (128 (node, group) rows) . K_idx_tile^T on the tensor
-// cores, so that one TMEM lane holds one row's 128 scores and the block maxima need no exchange between
-// lanes. Warps: 0-7 epilogue (two warpgroups take alternate accumulators of four), 8 TMA, 9 MMA. The
-// sequence's Q_idx rows are staged twice, so that the next sequence's load overlaps this one's tiles.
-// HBM-bound by design: each K_idx byte is read once for up to 256 rows. An SM gets a 16 KB tile every ~700
-// cycles from HBM; a 128 x 128 x 64 product is ~130, an accumulator's epilogue ~300 of one warpgroup.
+// ranges of all sequences' 256-token tiles. S = Q_idx (128 (node, group) rows) . K_idx_tile^T on the tensor
+// cores, so that one TMEM lane holds one row's scores and the block maxima need no exchange between lanes.
+// Warps: 0-7 epilogue, 8 TMA, 9 MMA. Each warpgroup of the epilogue owns one of two 256-column accumulators:
+// with more than 128 rows a row tile each, else alternate tiles. The sequence's Q_idx rows are staged twice, so
+// that the next sequence's load overlaps this one's tiles.
+// HBM-bound by design: each K_idx byte is read once for up to 256 rows. What else a tile costs is the issue of
+// one warp (waits, descriptors, commits): some 1000 cycles, as long as the 16 KB of a 128-token tile take to
+// arrive (1143 cycles a tile, 105 us for 16 x 262144 tokens); hence tiles of 256 tokens and warp-uniform loops.
 constexpr int kScanThreads = 320;
-constexpr int kAcc = 4;
+constexpr int kScanTile = 256;
 
 template <int DI>
 struct TreeScanSmem {
-    static constexpr int kStages = DI == 64 ? 8 : 16;
+    static constexpr int kStages = DI == 64 ? 4 : 8;
     alignas(1024) uint8_t q[2][2][kTile * DI * 2];
-    alignas(1024) uint8_t k[kStages][kTile * DI * 2];
-    uint64_t q_full[2], q_empty[2], k_full[kStages], k_empty[kStages], acc_full[kAcc], acc_empty[kAcc], drain;
-    unsigned long long anc[64];
-    int up[64];
+    alignas(1024) uint8_t k[kStages][kScanTile * DI * 2];
+    uint64_t q_full[2], q_empty[2], k_full[kStages], k_empty[kStages], acc_full[2], acc_empty[2], drain;
     uint32_t tmem_base;
 };
 
+__device__ __forceinline__ int scan_tiles(const TreeArgs& a, int b) {
+    return tree_nodes(a, b) > 0 ? (tree_len(a, b) + kScanTile - 1) / kScanTile : 0;
+}
 struct TileCursor {
-    int b, tile, n;  // tile `tile` of sequence b, which has n tiles
+    int b, tile, n, len;  // tile `tile` of sequence b, which has n tiles and len tokens
 };
 // Called by all lanes of a warp: the CTA's first tile and its number of tiles.
 __device__ int tile_range(const TreeArgs& a, TileCursor& c) {
@@ -70,12 +73,13 @@ __device__ int tile_range(const TreeArgs& a, TileCursor& c) {
             c.b = b0 + l;
             c.n = __shfl_sync(0xffffffffu, v, l);
             c.tile = (int)(lo - (cum + __shfl_sync(0xffffffffu, incl, l) - c.n));
+            c.len = tree_len(a, c.b);
             return (int)(hi - lo);
         }
         cum += __shfl_sync(0xffffffffu, incl, 31);
     }
     c.b = a.B;
-    c.tile = c.n = 0;
+    c.tile = c.n = c.len = 0;
     return 0;
 }
 // Moves to the next tile; true if it belongs to another sequence.
@@ -83,6 +87,7 @@ __device__ __forceinline__ bool tile_next(const TreeArgs& a, TileCursor& c) {
     if (++c.tile < c.n) return false;
     c.tile = 0;
     while (++c.b < a.B && (c.n = scan_tiles(a, c.b)) == 0) {}
+    if (c.b < a.B) c.len = tree_len(a, c.b);
     return true;
 }
 
@@ -92,29 +97,27 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 const __grid_constant__ TreeArgs a) {
     using Sm = TreeScanSmem<DI>;
     constexpr int kStages = Sm::kStages;
-    constexpr int TPT = kTile / BK;  // pages per tile
-    constexpr uint32_t kPageBytes = BK * DI * 2;
+    constexpr int TPT = kScanTile / BK;  // pages per tile
+    constexpr uint32_t kPageBytes = BK * DI * 2, kTileBytes = kScanTile * DI * 2, kQBytes = kTile * DI * 2;
     constexpr uint32_t kLayout = DI == 64 ? 2u : 4u;
     constexpr uint32_t kSBO = 8 * DI * 2;
-    constexpr uint32_t kIdesc = umma_idesc_bf16(kTile, kTile, false, false);
+    constexpr uint32_t kIdesc = umma_idesc_bf16(kTile, kScanTile, false, false);
     extern __shared__ uint8_t tree_raw[];
     Sm& s = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(tree_raw) + 1023) & ~uintptr_t(1023));
     const int warp = warp_id(), lane = lane_id();
-    const int R = a.T * a.H_kv;              // (node, group) rows of a sequence
+    const int R = a.T * a.H_kv;                             // (node, group) rows of a sequence
     const int row0 = blockIdx.y * 2 * kTile;
     const int rt = min(2, (R - row0 + kTile - 1) / kTile);  // row tiles of this CTA
     if (threadIdx.x == 0) {
         for (int x = 0; x < 2; ++x) {
             mbar_init(&s.q_full[x], 1);
             mbar_init(&s.q_empty[x], 1);
+            mbar_init(&s.acc_full[x], 1);
+            mbar_init(&s.acc_empty[x], 4);
         }
         for (int x = 0; x < kStages; ++x) {
             mbar_init(&s.k_full[x], 1);
             mbar_init(&s.k_empty[x], 1);
-        }
-        for (int x = 0; x < kAcc; ++x) {
-            mbar_init(&s.acc_full[x], 1);
-            mbar_init(&s.acc_empty[x], 4);
         }
         mbar_init(&s.drain, 1);
         fence_mbar_init();
@@ -123,146 +126,175 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         tmem_alloc(&s.tmem_base, 512);
         tmem_relinquish();
     }
+    TileCursor cur;
+    const int count = tile_range(a, cur);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s.tmem_base;
-    TileCursor cur;
-    const int count = tile_range(a, cur);
 
     if (warp == 8) {
         // ------------------------------------------------------------------------ TMA producer
+        const bool leader = elect_one();
         int n = 0, nq = -1, base = -32, page = 0;  // page: lane l holds the id of block base + l
+        int st = 0;
+        uint32_t ph = 1;  // parity that a stage's release has, before its first use the one that is already over
         bool fresh = true, ok = true;
-        for (; ok && n < count; ++n) {
+        for (; n < count; ++n) {
             if (fresh) {
                 ++nq;
-                if (lane == 0) {
-                    const int qs = nq & 1;
-                    ok = nq < 2 || mbar_wait(&s.q_empty[qs], ((nq >> 1) - 1) & 1, a.status, 0xb01);
-                    if (ok) {
-                        mbar_arrive_expect_tx(&s.q_full[qs], (uint32_t)rt * kTile * DI * 2);
-                        for (int x = 0; x < rt; ++x)
-                            tma_load_3d(s.q[qs][x], &tm_q, &s.q_full[qs], 0, row0 + x * kTile, cur.b);
-                    }
+                const int qs = nq & 1;
+                ok = nq < 2 || mbar_wait(&s.q_empty[qs], ((nq >> 1) - 1) & 1, a.status, 0xb01);
+                if (!ok) break;
+                if (leader) {
+                    mbar_arrive_expect_tx(&s.q_full[qs], (uint32_t)rt * kQBytes);
+                    for (int x = 0; x < rt; ++x) tma_load_3d(s.q[qs][x], &tm_q, &s.q_full[qs], 0, row0 + x * kTile, cur.b);
                 }
+                __syncwarp();
                 base = -32;
             }
             const int c0 = cur.tile * TPT;
-            const int blocks = (tree_len(a, cur.b) + BK - 1) / BK;
+            const int blocks = (cur.len + BK - 1) / BK;
             if (base < 0 || c0 >= base + 32) {  // TPT divides 32: a tile's pages never straddle a refill
                 base = c0 & ~31;
                 page = base + lane < blocks ? tree_page(a, cur.b, base + lane, 0xb02) : 0;
             }
-            const int np = min(TPT, blocks - c0), st = n % kStages;
-            if (lane == 0 && ok && n >= kStages) ok = mbar_wait(&s.k_empty[st], ((n / kStages) - 1) & 1, a.status, 0xb03);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&s.k_full[st], np * kPageBytes);
-            for (int x = 0; x < np; ++x) {
+            const int np = min(TPT, blocks - c0);
+            ok = mbar_wait(&s.k_empty[st], ph, a.status, 0xb03);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (leader) mbar_arrive_expect_tx(&s.k_full[st], np * kPageBytes);
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < TPT; ++x) {
                 const int p = __shfl_sync(0xffffffffu, page, (c0 + x) & 31);
-                if (lane == 0) tma_load_2d(s.k[st] + x * kPageBytes, &tm_k, &s.k_full[st], 0, p * BK);
+                if (leader && x < np) tma_load_2d(s.k[st] + x * kPageBytes, &tm_k, &s.k_full[st], 0, p * BK);
+            }
+            __syncwarp();
+            if (++st == kStages) {
+                st = 0;
+                ph ^= 1;
             }
             fresh = tile_next(a, cur);
         }
         // no copy of ours may still be landing when the CTA leaves
-        if (lane == 0) {
-            for (int m = max(0, n - kStages); m < n; ++m)
-                mbar_wait(&s.k_full[m % kStages], (m / kStages) & 1, a.status, 0xb04);
-            for (int m = max(0, nq - 1); m <= nq; ++m)
-                if (ok || m < nq) mbar_wait(&s.q_full[m & 1], (m >> 1) & 1, a.status, 0xb05);
-        }
+        for (int m = max(0, n - kStages); m < n; ++m)
+            mbar_wait(&s.k_full[m % kStages], (m / kStages) & 1, a.status, 0xb04);
+        for (int m = max(0, nq - 1); m <= nq; ++m)
+            if (ok || m < nq) mbar_wait(&s.q_full[m & 1], (m >> 1) & 1, a.status, 0xb05);
     } else if (warp == 9) {
         // ------------------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            int nq = -1, m = 0;
-            bool fresh = true, ok = true;
-            for (int n = 0; ok && n < count; ++n) {
-                if (fresh) {
-                    ++nq;
-                    ok = mbar_wait(&s.q_full[nq & 1], (nq >> 1) & 1, a.status, 0xb11);
-                }
-                const int st = n % kStages;
-                ok = ok && mbar_wait(&s.k_full[st], (n / kStages) & 1, a.status, 0xb12);
-                for (int x = 0; ok && x < rt; ++x, ++m) {
-                    const int acc = m % kAcc;
-                    if (m >= kAcc && !mbar_wait(&s.acc_empty[acc], ((m / kAcc) - 1) & 1, a.status, 0xb13)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t qb = smem_u32(s.q[nq & 1][x]), kb = smem_u32(s.k[st]);
+        const bool leader = elect_one();
+        const uint64_t dq = umma_sdesc(smem_u32(s.q[0][0]), 16, kSBO, kLayout), dk = umma_sdesc(smem_u32(s.k[0]), 16, kSBO, kLayout);
+        int nq = -1, st = 0;
+        uint32_t ph = 0;
+        bool fresh = true, ok = true;
+        for (int n = 0; ok && n < count; ++n) {
+            if (fresh) {
+                ++nq;
+                ok = mbar_wait(&s.q_full[nq & 1], (nq >> 1) & 1, a.status, 0xb11);
+            }
+            ok = ok && mbar_wait(&s.k_full[st], ph, a.status, 0xb12);
+            for (int x = 0; ok && x < rt; ++x) {
+                // accumulator: the row tile's, or alternate ones; use u of it waits for the release of use u - 1
+                const int acc = rt == 2 ? x : n & 1, u = rt == 2 ? n : n >> 1;
+                ok = mbar_wait(&s.acc_empty[acc], (u & 1) ^ 1, a.status, 0xb13);
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
+                    const uint64_t qd = dq + (((nq & 1) * 2 + x) * kQBytes >> 4), kd = dk + (st * kTileBytes >> 4);
 #pragma unroll
                     for (int ks = 0; ks < DI / 16; ++ks)
-                        umma_bf16(tmem + acc * kTile, umma_sdesc(qb + ks * 32, 16, kSBO, kLayout),
-                                  umma_sdesc(kb + ks * 32, 16, kSBO, kLayout), kIdesc, ks > 0);
+                        umma_bf16(tmem + acc * kScanTile, qd + 2 * ks, kd + 2 * ks, kIdesc, ks > 0);
                     umma_commit(&s.acc_full[acc]);
+                    if (x == rt - 1) umma_commit(&s.k_empty[st]);
                 }
-                if (!ok) break;
-                umma_commit(&s.k_empty[st]);
-                fresh = tile_next(a, cur);
-                if (fresh) umma_commit(&s.q_empty[nq & 1]);
+                __syncwarp();
             }
-            umma_commit(&s.drain);
-            mbar_wait(&s.drain, 0, a.status, 0xb14);
+            if (++st == kStages) {
+                st = 0;
+                ph ^= 1;
+            }
+            fresh = tile_next(a, cur);
+            if (fresh && leader) umma_commit(&s.q_empty[nq & 1]);
+            __syncwarp();
         }
+        if (leader) umma_commit(&s.drain);
+        mbar_wait(&s.drain, 0, a.status, 0xb14);
     } else {
         // ------------------------------------------------------------------------ epilogue
         const int wg = warp >> 2;
-        // the ancestor sets of the Top-k kernel, by the first two warps of the first CTAs
-        if (warp < 2 && blockIdx.y == 0)
-            for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-                const int nodes = tree_nodes(a, b);
-                tree_ancestors(a, b, nodes, s.anc, s.up, 1, 0xb21);
-                if ((int)threadIdx.x < nodes) a.anc[(int64_t)b * a.T + threadIdx.x] = s.anc[threadIdx.x];
-                bar_sync_named(1, 64);
-            }
-        const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const int nacc = count * rt;  // accumulators of the CTA; rt = 1: one per tile
-        if (rt == 1 && wg == 1 && count > 0) tile_next(a, cur);
-        for (int m = wg; m < nacc; m += 2) {
-            const int acc = m % kAcc;
-            const bool got = mbar_wait(&s.acc_full[acc], (m / kAcc) & 1, a.status, 0xb22);
-            if (!__all_sync(0xffffffffu, got)) break;
+        const uint32_t tacc = tmem + ((uint32_t)((warp & 3) * 32) << 16) + wg * kScanTile;
+        const int row = row0 + (rt == 2 ? wg * kTile : 0) + (warp & 3) * 32 + lane;
+        const int step = rt == 2 ? 1 : 2;  // tiles between this warpgroup's
+        if (step == 2 && wg == 1 && count > 1) tile_next(a, cur);
+        uint32_t ph = 0;
+        for (int n = step == 2 ? wg : 0; n < count; n += step) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&s.acc_full[wg], ph, a.status, 0xb22))) break;
+            ph ^= 1;
             tc_fence_after();
-            const int row = row0 + (rt == 2 ? wg * kTile : 0) + (warp & 3) * 32 + lane;
+            float cmax[8];  // maxima of 32-column chunks
             if (row - lane < R) {
-                const int left = tree_len(a, cur.b) - cur.tile * kTile;  // keys of the tile that exist
-                uint32_t v[4][32];
+                const int left = cur.len - cur.tile * kScanTile;  // keys of the tile that exist
 #pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_ld32(lane_addr + acc * kTile + q * 32, v[q]);
-                tmem_ld_wait();
-                float cmax[4];
+                for (int hf = 0; hf < 4; ++hf) {
+                    uint32_t v[2][32];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    reg_fence(v[q]);
-                    float* f = reinterpret_cast<float*>(v[q]);
-                    if (left < kTile) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] = q * 32 + e < left ? f[e] : -INFINITY;
+                    for (int q = 0; q < 2; ++q) tmem_ld32(tacc + hf * 64 + q * 32, v[q]);
+                    tmem_ld_wait();
+                    if (hf == 3) {  // the accumulator is read: the next product may start
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s.acc_empty[wg]);
                     }
-                    float m0 = max3f(f[0], f[1], f[2]), m1 = max3f(f[3], f[4], f[5]);
 #pragma unroll
-                    for (int e = 6; e < 30; e += 4) {
-                        m0 = max3f(m0, f[e], f[e + 1]);
-                        m1 = max3f(m1, f[e + 2], f[e + 3]);
+                    for (int q = 0; q < 2; ++q) {
+                        reg_fence(v[q]);
+                        float* f = reinterpret_cast<float*>(v[q]);
+                        if (left < kScanTile) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) f[e] = hf * 64 + q * 32 + e < left ? f[e] : -INFINITY;
+                        }
+                        float m0 = max3f(f[0], f[1], f[2]), m1 = max3f(f[3], f[4], f[5]);
+#pragma unroll
+                        for (int e = 6; e < 30; e += 4) {
+                            m0 = max3f(m0, f[e], f[e + 1]);
+                            m1 = max3f(m1, f[e + 2], f[e + 3]);
+                        }
+                        cmax[hf * 2 + q] = max3f(m0, m1, fmaxf(f[30], f[31]));
                     }
-                    cmax[q] = max3f(m0, m1, fmaxf(f[30], f[31]));
                 }
                 if (row < R) {
                     float* out = a.bmax + ((int64_t)cur.b * R + row) * a.bmax_ld + cur.tile * TPT;
-                    if constexpr (TPT == 4) *reinterpret_cast<float4*>(out) = make_float4(cmax[0], cmax[1], cmax[2], cmax[3]);
-                    if constexpr (TPT == 2)
-                        *reinterpret_cast<float2*>(out) = make_float2(fmaxf(cmax[0], cmax[1]), fmaxf(cmax[2], cmax[3]));
-                    if constexpr (TPT == 1) *out = fmaxf(fmaxf(cmax[0], cmax[1]), fmaxf(cmax[2], cmax[3]));
+                    if constexpr (TPT == 8) {
+                        reinterpret_cast<float4*>(out)[0] = make_float4(cmax[0], cmax[1], cmax[2], cmax[3]);
+                        reinterpret_cast<float4*>(out)[1] = make_float4(cmax[4], cmax[5], cmax[6], cmax[7]);
+                    } else if constexpr (TPT == 4) {
+                        *reinterpret_cast<float4*>(out) = make_float4(fmaxf(cmax[0], cmax[1]), fmaxf(cmax[2], cmax[3]),
+                                                                      fmaxf(cmax[4], cmax[5]), fmaxf(cmax[6], cmax[7]));
+                    } else {
+                        *reinterpret_cast<float2*>(out) =
+                            make_float2(fmaxf(fmaxf(cmax[0], cmax[1]), fmaxf(cmax[2], cmax[3])),
+                                        fmaxf(fmaxf(cmax[4], cmax[5]), fmaxf(cmax[6], cmax[7])));
+                    }
                 }
+            } else {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.acc_empty[wg]);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.acc_empty[acc]);
             tile_next(a, cur);
-            if (rt == 1 && m + 2 < nacc) tile_next(a, cur);
+            if (step == 2 && n + 2 < count) tile_next(a, cur);
         }
+        // the ancestor sets of the Top-k kernel
+        if (warp == 7 && blockIdx.y == 0)
+            for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+                const int nodes = tree_nodes(a, b);
+                unsigned long long anc[2];
+                tree_ancestors(a, nodes, load_parent(a, b, lane), load_parent(a, b, lane + 32), anc, 0xb21);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (lane + 32 * x < nodes) a.anc[(int64_t)b * a.T + lane + 32 * x] = anc[x];
+            }
     }
     tc_fence_before();
     __syncthreads();
@@ -424,12 +456,12 @@ __global__ void __launch_bounds__(kTopkWarps * 32) k_tree_topk(const __grid_cons
 }  // namespace
 
 size_t tree_index_ws_bytes(int B, int N, int H_kv, int block_k, int T) {
-    const size_t ld = ((size_t)(N + kTile - 1) / kTile) * (kTile / block_k);
+    const size_t ld = ((size_t)(N + kScanTile - 1) / kScanTile) * (kScanTile / block_k);
     auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
     return al((size_t)B * T * 8) + al((size_t)B * T * H_kv * ((ld + 3) / 4 * 4) * 4);
 }
 void tree_index_carve(TreeArgs* a, void* base) {
-    const int ld = ((a->N + kTile - 1) / kTile) * (kTile / a->block_k);
+    const int ld = ((a->N + kScanTile - 1) / kScanTile) * (kScanTile / a->block_k);
     a->bmax_ld = (ld + 3) / 4 * 4;
     a->anc = static_cast<unsigned long long*>(base);
     a->bmax = reinterpret_cast<float*>(static_cast<uint8_t*>(base) + (((size_t)a->B * a->T * 8 + 255) & ~size_t(255)));

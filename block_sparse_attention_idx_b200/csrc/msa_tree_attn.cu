@@ -31,33 +31,47 @@ constexpr int kWords = kTreeMaxBlocks / 32;
 
 template <int D, int NWG>
 struct TreeAttnSmem {
-    alignas(1024) uint8_t q[NWG][kRows * D * 2];
+    alignas(1024) uint8_t q[NWG][kRows * D * 2];  // at the end, with the start of k: the outputs on their way out
     alignas(1024) uint8_t k[2][kTile * D * 2];
     alignas(1024) uint8_t v[2][kTile * D * 2];
     unsigned long long mask[kMaxEntries];   // nodes of the CTA that chose the entry
     unsigned long long anc[64], draft[64];  // ancestors of a node; drafted tokens that a node attends
+    unsigned long long in_block[4];         // nodes whose position lies in block len / block_k + i
     int page[kMaxEntries];
-    int up[64];
+    int local[64];                          // local block of a node
     uint32_t late[64];                      // blocks >= len / block_k in a node's list
     uint32_t bits[kWords];
     int before[kWords];
     // s_full and p_ready: one per S buffer. A warp whose rows are masked runs ahead of the others, by one tile at
     // most, and must not arrive twice on one barrier for them.
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], pv_done[2], drain;
-    int total, last_partial;
+    int total;
     uint32_t tmem_base;
 };
 
+// Threads: the softmax warpgroups, then a TMA and an MMA warp. With NWG = 2 these two are part of a third
+// warpgroup (two of its warps only help in the prologue) that gives up registers: 384 threads start with 168
+// each (64512), 128 of them drop to 72 and 256 rise to 216 (9216 + 55296 = 64512), so that a row's 128 scores
+// stay in registers.
+constexpr int attn_threads(int nwg) { return nwg == 2 ? 384 : 192; }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 template <int D, int BK, int NWG>
-__global__ void __launch_bounds__((4 * NWG + 2) * 32, 1)
+__global__ void __launch_bounds__(attn_threads(NWG), 1)
     k_tree_attn(const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
                 const __grid_constant__ CUtensorMap tm_kd, const __grid_constant__ CUtensorMap tm_vd,
                 const __grid_constant__ TreeArgs a, const __nv_bfloat16* __restrict__ q) {
     using Sm = TreeAttnSmem<D, NWG>;
     constexpr int TPT = kTile / BK;
-    constexpr int NT = (4 * NWG + 2) * 32;
+    constexpr int NT = attn_threads(NWG);
+    constexpr int kTmaWarp = 4 * NWG, kMmaWarp = 4 * NWG + 1;
     constexpr uint32_t kHalf = kTile * 128;  // bytes of a 64-column half of a 128-row tile
+    constexpr uint32_t kTileBytes = kTile * D * 2;
     constexpr int kColO = 256;
+    constexpr int EPT = (kMaxEntries + NT - 1) / NT;  // list entries per thread
     extern __shared__ uint8_t tree_raw[];
     Sm& s = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(tree_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
@@ -66,18 +80,39 @@ __global__ void __launch_bounds__((4 * NWG + 2) * 32, 1)
     const int n_ct = (a.T + per_cta - 1) / per_cta;
     const int ct = blockIdx.x % n_ct, br = blockIdx.x / n_ct, r = br % a.H_kv, b = br / a.H_kv;
     const int split = blockIdx.y, n0 = ct * per_cta;
-    const int len = tree_len(a, b), nodes = tree_nodes(a, b);
-    const int full = len / BK, npages = (len + BK - 1) / BK;  // complete pages, pages
     const int64_t n_rows = (int64_t)a.B * a.T * a.H_q;
-    if (tid == 0 && r == 0 && ct == 0 && split == 0 && (len != a.cache_len[b] || nodes != a.n_nodes[b]))
-        raise_flag(a.status, MSA_DEV_BAD_BLOCK, 0xc01);
 
     // ------------------------------------------------------------------ the union of the CTA's lists
-    if (tid < 64) tree_ancestors(a, b, nodes, s.anc, s.up, 1, 0xc02);
+    // Loads that depend on nothing go first: the lists (kept in registers), the parents, Q. Rows of nodes that
+    // do not exist are loaded too: nothing they hold reaches another row, and they see no key.
+    int id[EPT], pg[EPT];
+    const int n_ent = min(per_cta, a.T - n0) * K1;
+#pragma unroll
+    for (int x = 0; x < EPT; ++x) {
+        const int e = tid + x * NT;
+        id[x] = e < n_ent ? a.blocks[(((int64_t)b * a.T + n0 + e / K1) * a.H_kv + r) * K1 + e % K1] : -1;
+    }
+    int p0 = -1, p1 = -1;
+    if (warp == kTmaWarp) {
+        p0 = load_parent(a, b, lane);
+        p1 = load_parent(a, b, lane + 32);
+    }
+    const int len = tree_len(a, b), nodes = tree_nodes(a, b);
+    for (int i = tid; i < NWG * kRows * (D / 8); i += NT) {
+        const int row = i / (D / 8), c = i % (D / 8), node = n0 + row / G, h = row % G;
+        const uint32_t dst = smem_u32(s.q[0]) + (row / kRows) * (kRows * D * 2) + (c / 8) * kHalf +
+                             swz(row % kRows, (c % 8) * 16, 128);
+        const bool live = node < a.T;
+        cp_async_16_zfill(dst, live ? q + (((int64_t)b * a.T + node) * a.H_q + r * G + h) * D + c * 8 : q, live);
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&s.tmem_base, 512);
+        tmem_relinquish();
+    }
     for (int i = tid; i < kWords; i += NT) s.bits[i] = 0u;
     for (int i = tid; i < kMaxEntries; i += NT) s.mask[i] = 0ull;
     if (tid < 64) s.late[tid] = 0u;
-    if (tid == 0) {
+    if (tid == 64) {
         for (int x = 0; x < 2; ++x) {
             mbar_init(&s.k_full[x], 1);
             mbar_init(&s.k_empty[x], 1);
@@ -90,30 +125,50 @@ __global__ void __launch_bounds__((4 * NWG + 2) * 32, 1)
         mbar_init(&s.drain, 1);
         fence_mbar_init();
     }
-    // Q rows (zero where the node does not exist), swizzled halves of 64 columns
-    for (int i = tid; i < NWG * kRows * (D / 8); i += NT) {
-        const int row = i / (D / 8), c = i % (D / 8), node = n0 + row / G, h = row % G;
-        const uint32_t dst = smem_u32(s.q[0]) + (row / kRows) * (kRows * D * 2) + (c / 8) * kHalf +
-                             swz(row % kRows, (c % 8) * 16, 128);
-        const bool live = node < nodes;
-        cp_async_16_zfill(dst, live ? q + (((int64_t)b * a.T + node) * a.H_q + r * G + h) * D + c * 8 : q, live);
-    }
-    if (warp == 4 * NWG + 1) {
-        tmem_alloc(&s.tmem_base, 512);
-        tmem_relinquish();
+    const int full = len / BK, npages = (len + BK - 1) / BK;  // complete pages, pages
+    if (warp == kTmaWarp) {
+        if (lane == 0) {
+            prefetch_tmap(&tm_kp);
+            prefetch_tmap(&tm_vp);
+            if (r == 0 && ct == 0 && split == 0 && (len != a.cache_len[b] || nodes != a.n_nodes[b]))
+                raise_flag(a.status, MSA_DEV_BAD_BLOCK, 0xc01);
+        }
+        unsigned long long anc[2];
+        tree_ancestors(a, nodes, p0, p1, anc, 0xc02);
+        int off[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int n = lane + 32 * x, loc = (len + __popcll(anc[x]) - 1) / BK;
+            s.anc[n] = anc[x];
+            s.local[n] = loc;
+            off[x] = n < nodes ? loc - full : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = __ballot_sync(0xffffffffu, off[0] == i), hi = __ballot_sync(0xffffffffu, off[1] == i);
+            if (lane == 0) s.in_block[i] = ((unsigned long long)hi << 32) | lo;
+        }
     }
     __syncthreads();
     const int mine = max(0, min(per_cta, nodes - n0));  // nodes of this CTA that exist
-    for (int e = tid; e < mine * K1; e += NT) {
-        const int nl = e / K1, n = n0 + nl;
-        const int c = a.blocks[(((int64_t)b * a.T + n) * a.H_kv + r) * K1 + e % K1];
-        if (c == -1) continue;
-        if (c < -1 || c > (len + __popcll(s.anc[n]) - 1) / BK) {
+#pragma unroll
+    for (int x = 0; x < EPT; ++x) {
+        const int e = tid + x * NT, nl = e / K1;
+        pg[x] = 0;
+        if (id[x] == -1 || nl >= mine) {
+            id[x] = -1;
+        } else if (id[x] < -1 || id[x] > s.local[n0 + nl]) {
             raise_flag(a.status, MSA_DEV_BAD_BLOCK, 0xc03);
-            continue;
+            id[x] = -1;
+        } else {
+            if (id[x] >= full) atomicOr(&s.late[nl], 1u << (id[x] - full));
+            if (id[x] < npages) {
+                atomicOr(&s.bits[id[x] >> 5], 1u << (id[x] & 31));
+                pg[x] = tree_page(a, b, id[x], 0xc04);
+            } else {
+                id[x] = -1;
+            }
         }
-        if (c < npages) atomicOr(&s.bits[c >> 5], 1u << (c & 31));
-        if (c >= full) atomicOr(&s.late[nl], 1u << (c - full));
     }
     __syncthreads();
     if (warp == 0) {
@@ -133,18 +188,15 @@ __global__ void __launch_bounds__((4 * NWG + 2) * 32, 1)
             at += __popc(s.bits[lane * (kWords / 32) + x]);
         }
         if (lane == 31) s.total = incl;
-        if (lane == 0) s.last_partial = npages > full && ((s.bits[full >> 5] >> (full & 31)) & 1);
-    }
-    if (tid >= 64 && tid - 64 < mine) {
-        // drafted tokens that node n0 + tid - 64 attends: its ancestors in its selected blocks
+    } else if (tid >= 64 && tid < 128) {
+        // drafted tokens that a node attends: its ancestors in its selected blocks
         const int nl = tid - 64;
-        unsigned long long left = s.anc[n0 + nl], d = 0ull;
-        const uint32_t late = s.late[nl];
-        while (left) {
-            const int m = __ffsll(left) - 1;
-            left &= left - 1;
-            const int c = (len + __popcll(s.anc[m]) - 1) / BK;
-            if ((late >> (c - full)) & 1) d |= 1ull << m;
+        unsigned long long d = 0ull;
+        if (nl < mine) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if ((s.late[nl] >> i) & 1) d |= s.in_block[i];
+            d &= s.anc[n0 + nl];
         }
         s.draft[nl] = d;
     }
@@ -153,17 +205,20 @@ __global__ void __launch_bounds__((4 * NWG + 2) * 32, 1)
     const int page_tiles = (U + TPT - 1) / TPT;
     // tiles of this split: page tiles, then the drafted tokens' tile; none where the CTA has no nodes
     const int tiles = mine > 0 ? page_tiles + 1 : 0;
-    const int t0 = (int)((int64_t)tiles * split / a.splits), t1 = (int)((int64_t)tiles * (split + 1) / a.splits);
+    const int t0 = tiles * split / a.splits, t1 = tiles * (split + 1) / a.splits;
     const int e_lo = t0 * TPT, e_hi = min(U, t1 * TPT);
-    for (int e = tid; e < mine * K1; e += NT) {
-        const int nl = e / K1, n = n0 + nl;
-        const int c = a.blocks[(((int64_t)b * a.T + n) * a.H_kv + r) * K1 + e % K1];
-        if (c < 0 || c >= npages || c > (len + __popcll(s.anc[n]) - 1) / BK) continue;
-        const int x = s.before[c >> 5] + __popc(s.bits[c >> 5] & ((1u << (c & 31)) - 1u));
-        if (x < e_lo || x >= e_hi) continue;
-        atomicOr(&s.mask[x - e_lo], 1ull << nl);
-        s.page[x - e_lo] = tree_page(a, b, c, 0xc04);
+#pragma unroll
+    for (int x = 0; x < EPT; ++x) {
+        if (id[x] < 0) continue;
+        const int c = id[x], at = s.before[c >> 5] + __popc(s.bits[c >> 5] & ((1u << (c & 31)) - 1u));
+        if (at < e_lo || at >= e_hi) continue;
+        atomicOr(&s.mask[at - e_lo], 1ull << ((tid + x * NT) / K1));
+        s.page[at - e_lo] = pg[x];
     }
+    // keys of the last page tile: the cache's last page, if chosen, holds len % block_k
+    const bool partial = npages > full && ((s.bits[full >> 5] >> (full & 31)) & 1);
+    const int last_keys = (U - (page_tiles - 1) * TPT) * BK - (partial ? BK - len % BK : 0);
+    auto tile_keys = [&](int t) { return t < page_tiles - 1 ? kTile : t < page_tiles ? last_keys : nodes; };
     cp_async_wait_all();
     fence_proxy_async();
     tc_fence_before();
@@ -171,130 +226,154 @@ __global__ void __launch_bounds__((4 * NWG + 2) * 32, 1)
     tc_fence_after();
     const uint32_t tmem = s.tmem_base;
     const int n_tiles = t1 - t0;
-    // keys of local tile j: pages hold block_k each, the cache's last page len % block_k, the last tile the nodes
-    auto tile_keys = [&](int j) {
-        const int t = t0 + j;
-        if (t == page_tiles) return nodes;
-        const int cnt = min(TPT, U - t * TPT);
-        return t == page_tiles - 1 && s.last_partial ? (cnt - 1) * BK + len % BK : cnt * BK;
-    };
 
-    if (warp == 4 * NWG) {
+    if (warp >= kTmaWarp) {
+    if constexpr (NWG == 2) regs_dec<72>();
+    if (warp == kTmaWarp) {
         // -------------------------------------------------------------------- TMA producer
-        if (lane == 0) {
-            int j = 0;
-            bool ok = true;
-            for (; j < n_tiles; ++j) {
-                const int st = j & 1, t = t0 + j;
-                const bool drafted = t == page_tiles;
-                const int cnt = drafted ? 1 : min(TPT, U - t * TPT);
-                const uint32_t bytes = drafted ? 64u * D * 2 : (uint32_t)cnt * BK * D * 2;
-                for (int kv = 0; kv < 2 && ok; ++kv) {
-                    uint64_t* fullb = kv ? &s.v_full[st] : &s.k_full[st];
-                    if (j >= 2 && !mbar_wait(kv ? &s.v_empty[st] : &s.k_empty[st], ((j >> 1) - 1) & 1, a.status, 0xc11)) {
-                        ok = false;
-                        break;
-                    }
+        const bool leader = elect_one();
+        int j = 0;
+        bool ok = true;
+        for (; j < n_tiles; ++j) {
+            const int st = j & 1, t = t0 + j;
+            const bool drafted = t == page_tiles;
+            const int cnt = drafted ? 1 : min(TPT, U - t * TPT);
+            const uint32_t bytes = drafted ? 64u * D * 2 : (uint32_t)cnt * BK * D * 2;
+            int rows[TPT];
+#pragma unroll
+            for (int x = 0; x < TPT; ++x) rows[x] = x < cnt && !drafted ? s.page[t * TPT + x - e_lo] * BK : 0;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                uint64_t* fullb = kv ? &s.v_full[st] : &s.k_full[st];
+                if (ok && j >= 2) ok = mbar_wait(kv ? &s.v_empty[st] : &s.k_empty[st], ((j >> 1) - 1) & 1, a.status, 0xc11);
+                if (!ok) break;
+                if (leader) {
                     uint8_t* dst = kv ? s.v[st] : s.k[st];
                     mbar_arrive_expect_tx(fullb, bytes);
 #pragma unroll
                     for (int h = 0; h < D / 64; ++h) {
-                        if (drafted)
+                        if (drafted) {
                             tma_load_4d(dst + h * kHalf, kv ? &tm_vd : &tm_kd, fullb, 64 * h, r, 0, b);
-                        else
-                            for (int x = 0; x < cnt; ++x)
-                                tma_load_3d(dst + h * kHalf + x * BK * 128, kv ? &tm_vp : &tm_kp, fullb, 64 * h, r,
-                                            s.page[t * TPT + x - e_lo] * BK);
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < TPT; ++x)
+                                if (x < cnt)
+                                    tma_load_3d(dst + h * kHalf + x * BK * 128, kv ? &tm_vp : &tm_kp, fullb, 64 * h, r, rows[x]);
+                        }
                     }
                 }
-                if (!ok) break;
+                __syncwarp();
             }
-            // no copy of ours may still be landing when the CTA leaves
-            for (int m = max(0, j - 2); m < j; ++m) {
-                mbar_wait(&s.k_full[m & 1], (m >> 1) & 1, a.status, 0xc12);
-                mbar_wait(&s.v_full[m & 1], (m >> 1) & 1, a.status, 0xc13);
-            }
+            if (!ok) break;
         }
-    } else if (warp == 4 * NWG + 1) {
+        // no copy of ours may still be landing when the CTA leaves
+        for (int m = max(0, j - 2); m < j; ++m) {
+            mbar_wait(&s.k_full[m & 1], (m >> 1) & 1, a.status, 0xc12);
+            mbar_wait(&s.v_full[m & 1], (m >> 1) & 1, a.status, 0xc13);
+        }
+    } else if (warp == kMmaWarp) {
         // -------------------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            auto issue_s = [&](int w, int j) {
-                const uint32_t nk = (uint32_t)(tile_keys(j) + 15) & ~15u;
-                const uint32_t idesc = umma_idesc_bf16(kRows, 0, false, false) | ((nk >> 3) << 17);
-                const uint32_t qb = smem_u32(s.q[w]), kb = smem_u32(s.k[j & 1]);
-                const int buf = NWG == 1 ? (j & 1) : w;
+        const bool leader = elect_one();
+        const uint64_t dq = umma_sdesc(smem_u32(s.q[0]), 16, 1024, 2), dk = umma_sdesc(smem_u32(s.k[0]), 16, 1024, 2);
+        const uint64_t dv = umma_sdesc(smem_u32(s.v[0]), kHalf, 1024, 2);
+        auto issue_s = [&](int w, int j) {
+            const uint32_t nk = (uint32_t)(tile_keys(t0 + j) + 15) & ~15u;
+            const uint32_t idesc = umma_idesc_bf16(kRows, 0, false, false) | ((nk >> 3) << 17);
+            const int buf = NWG == 1 ? (j & 1) : w;
+            if (leader) {
+                const uint64_t qd = dq + w * (kTileBytes >> 4), kd = dk + (j & 1) * (kTileBytes >> 4);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks / 4) * kHalf + (ks & 3) * 32;
-                    umma_bf16(tmem + buf * kTile, umma_sdesc(qb + off, 16, 1024, 2), umma_sdesc(kb + off, 16, 1024, 2),
-                              idesc, ks > 0);
+                    const uint32_t off = ((ks / 4) * kHalf + (ks & 3) * 32) >> 4;
+                    umma_bf16(tmem + buf * kTile, qd + off, kd + off, idesc, ks > 0);
                 }
                 umma_commit(&s.s_full[buf]);
                 if (w == NWG - 1) umma_commit(&s.k_empty[j & 1]);
-            };
-            constexpr uint32_t kIdescO = umma_idesc_bf16(kRows, D, false, true);
-            bool ok = true;
-            if (n_tiles > 0) {
-                ok = mbar_wait(&s.k_full[0], 0, a.status, 0xc21);
-                tc_fence_after();
-                for (int w = 0; ok && w < NWG; ++w) issue_s(w, 0);
             }
-            for (int j = 0; ok && j < n_tiles; ++j) {
-                const bool more = j + 1 < n_tiles;
-                if (more) ok = mbar_wait(&s.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, a.status, 0xc22);
-                if (NWG == 1 && ok && more) {
-                    tc_fence_after();
-                    issue_s(0, j + 1);
-                }
-                ok = ok && mbar_wait(&s.v_full[j & 1], (j >> 1) & 1, a.status, 0xc23);
-                const int steps = (tile_keys(j) + 15) / 16;
-                for (int w = 0; ok && w < NWG; ++w) {
-                    ok = mbar_wait(&s.p_ready[NWG == 1 ? (j & 1) : w], (NWG == 1 ? j >> 1 : j) & 1, a.status, 0xc24);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t tP = tmem + (NWG == 1 ? (j & 1) : w) * kTile, vb = smem_u32(s.v[j & 1]);
-                    for (int ks = 0; ks < steps; ++ks)
-                        umma_bf16_tmem_a(tmem + kColO + w * kRows, tP + 8 * ks, umma_sdesc(vb + ks * 16 * 128, kHalf, 1024, 2),
-                                         kIdescO, j > 0 || ks > 0);
+            __syncwarp();
+        };
+        constexpr uint32_t kIdescO = umma_idesc_bf16(kRows, D, false, true);
+        bool ok = true;
+        if (n_tiles > 0) {
+            ok = mbar_wait(&s.k_full[0], 0, a.status, 0xc21);
+            tc_fence_after();
+#pragma unroll
+            for (int w = 0; w < NWG; ++w)
+                if (ok) issue_s(w, 0);
+        }
+        for (int j = 0; ok && j < n_tiles; ++j) {
+            const bool more = j + 1 < n_tiles;
+            if (more) ok = mbar_wait(&s.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, a.status, 0xc22);
+            if (NWG == 1 && ok && more) {
+                tc_fence_after();
+                issue_s(0, j + 1);
+            }
+            ok = ok && mbar_wait(&s.v_full[j & 1], (j >> 1) & 1, a.status, 0xc23);
+            const int steps = (tile_keys(t0 + j) + 15) / 16;
+#pragma unroll
+            for (int w = 0; w < NWG; ++w) {
+                const int buf = NWG == 1 ? (j & 1) : w;
+                ok = ok && mbar_wait(&s.p_ready[buf], (NWG == 1 ? j >> 1 : j) & 1, a.status, 0xc24);
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t tP = tmem + buf * kTile, tO = tmem + kColO + w * kRows;
+                    const uint64_t vd = dv + (j & 1) * (kTileBytes >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < kTile / 16; ++ks)
+                        if (ks < steps) umma_bf16_tmem_a(tO, tP + 8 * ks, vd + ((ks * 16 * 128) >> 4), kIdescO, j > 0 || ks > 0);
                     umma_commit(&s.pv_done[w]);
                     if (w == NWG - 1) umma_commit(&s.v_empty[j & 1]);
-                    if (NWG == 2 && more) issue_s(w, j + 1);
                 }
+                __syncwarp();
+                if (NWG == 2 && more) issue_s(w, j + 1);
             }
-            umma_commit(&s.drain);
-            mbar_wait(&s.drain, 0, a.status, 0xc25);
         }
+        if (leader) umma_commit(&s.drain);
+        mbar_wait(&s.drain, 0, a.status, 0xc25);
+    }
     } else {
+        if constexpr (NWG == 2) regs_inc<216>();
         // -------------------------------------------------------------------- softmax: one row per thread
         const int w = warp >> 2, row = (warp & 3) * 32 + lane;
-        const int nl = (w * kRows + row) / G, h = (w * kRows + row) % G;
+        const int nl = (w * kRows + row) / G;
         const bool live = nl < mine;
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t tO = lane_addr + kColO + w * kRows;
         const float sl2 = a.scale * 1.4426950408889634f;
-        const unsigned long long draft = live ? s.draft[nl] : 0ull;
-        float mref = -INFINITY, l = 0.f, lr = 0.f;
+        const uint64_t sl2x2 = f2_packf(sl2, sl2);
+        const uint32_t* my_mask = reinterpret_cast<const uint32_t*>(s.mask) + ((nl >> 5) & 1);  // this row's word of an entry
+        const uint32_t my_bit = live ? 1u << (nl & 31) : 0u;
+        float mref = -INFINITY;
+        uint64_t l2 = f2_packf(0.f, 0.f), lr2 = l2;  // the row's sum and that of the rounded P, two halves each
         bool ok = true;
         for (int j = 0; j < n_tiles; ++j) {
-            const int t = t0 + j, keys = tile_keys(j), buf = NWG == 1 ? (j & 1) : w;
-            // columns of each 32-column chunk that this row sees
+            const int t = t0 + j, keys = tile_keys(t), buf = NWG == 1 ? (j & 1) : w;
+            const bool whole = t < page_tiles && keys == kTile;  // every column is a cached key
+            // chunks of 32 columns that this row sees, as all-ones or zero words; in a tile that is not whole the
+            // columns one by one
             uint32_t see[4];
+            if (t < page_tiles) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (t == page_tiles) {
-                    see[c] = c < 2 ? (uint32_t)(draft >> (32 * c)) : 0u;
-                } else {
-                    const int left = keys - 32 * c;  // keys in this chunk
-                    const uint32_t there = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
-                    const int e = t * TPT + c / (BK / 32) - e_lo;
-                    see[c] = live && left > 0 && ((s.mask[e] >> nl) & 1) ? there : 0u;
+                for (int c = 0; c < 4; ++c) {
+                    const int e = c / (BK / 32);
+                    see[c] = t * TPT + e < U && (my_mask[2 * (t * TPT + e - e_lo)] & my_bit) ? 0xffffffffu : 0u;
+                    if (!whole) {
+                        const int left = keys - 32 * c;  // keys in this chunk
+                        see[c] &= left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+                    }
                 }
+            } else {
+                const unsigned long long d = live ? s.draft[nl] : 0ull;
+                see[0] = (uint32_t)d;
+                see[1] = (uint32_t)(d >> 32);
+                see[2] = see[3] = 0u;
             }
             // rows of V behind the tile's last key, up to the product's depth, hold whatever the page or the
             // stage held before: zeros, so that P = 0 there gives 0 even against NaN
             const int pad = ((keys + 15) & ~15) - keys;
             if (w == 0 && pad) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&s.v_full[j & 1], (j >> 1) & 1, a.status, 0xc31))) ok = false;
+                ok = __all_sync(0xffffffffu, mbar_wait(&s.v_full[j & 1], (j >> 1) & 1, a.status, 0xc31));
                 for (int i = row; ok && i < pad * (D / 8); i += kRows) {
                     const int vr = keys + i / (D / 8), c = i % (D / 8);
                     *reinterpret_cast<uint4*>(s.v[j & 1] + (c / 8) * kHalf + swz(vr, (c % 8) * 16, 128)) = make_uint4(0, 0, 0, 0);
@@ -305,8 +384,7 @@ __global__ void __launch_bounds__((4 * NWG + 2) * 32, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t tS = lane_addr + buf * kTile;
-            const bool any = __any_sync(0xffffffffu, (see[0] | see[1] | see[2] | see[3]) != 0u);
-            if (!any) {
+            if (!__any_sync(0xffffffffu, (see[0] | see[1] | see[2] | see[3]) != 0u)) {
                 uint32_t z[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) z[i] = 0u;
@@ -317,7 +395,6 @@ __global__ void __launch_bounds__((4 * NWG + 2) * 32, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, x[c]);
                 tmem_ld_wait();
-                const bool whole = __all_sync(0xffffffffu, (see[0] & see[1] & see[2] & see[3]) == 0xffffffffu);
                 float mx = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -333,7 +410,8 @@ __global__ void __launch_bounds__((4 * NWG + 2) * 32, 1)
                         m0 = max3f(m0, f[e], f[e + 1]);
                         m1 = max3f(m1, f[e + 2], f[e + 3]);
                     }
-                    mx = fmaxf(mx, max3f(m0, m1, fmaxf(f[30], f[31])));
+                    m0 = max3f(m0, m1, fmaxf(f[30], f[31]));
+                    mx = see[c] ? fmaxf(mx, m0) : mx;
                 }
                 mx *= sl2;
                 if (j == 0) {
@@ -346,8 +424,8 @@ __global__ void __launch_bounds__((4 * NWG + 2) * 32, 1)
                         tc_fence_after();
                         const float f = up ? fast_exp2(mref - mx) : 1.f;
                         if (up) mref = mx;
-                        l *= f;
-                        lr *= f;
+                        l2 = f2_mul(l2, f2_packf(f, f));
+                        lr2 = f2_mul(lr2, f2_packf(f, f));
 #pragma unroll
                         for (int c = 0; c < D / 16; ++c) {
                             uint32_t o[16];
@@ -361,17 +439,24 @@ __global__ void __launch_bounds__((4 * NWG + 2) * 32, 1)
                     }
                 }
                 const float base = mref == -INFINITY ? 0.f : mref;
+                const uint64_t nb2 = f2_packf(-base, -base);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const float* f = reinterpret_cast<const float*>(x[c]);
+                    // a chunk that the row does not see in a whole tile: its P and its part of the sum are dropped
+                    const uint32_t keep = whole ? see[c] : 0xffffffffu;
                     uint32_t pk[16];
+                    uint64_t sum = f2_packf(0.f, 0.f), sumr = sum;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float p0 = fast_exp2(fmaf(f[2 * e], sl2, -base)), p1 = fast_exp2(fmaf(f[2 * e + 1], sl2, -base));
-                        l += p0 + p1;
-                        pk[e] = pack_bf16x2(p0, p1);
-                        lr += __uint_as_float(pk[e] << 16) + __uint_as_float(pk[e] & 0xffff0000u);
+                        float z0, z1;
+                        f2_unpack(f2_fma(f2_pack(x[c][2 * e], x[c][2 * e + 1]), sl2x2, nb2), z0, z1);
+                        const float e0 = fast_exp2(z0), e1 = fast_exp2(z1);
+                        sum = f2_add(sum, f2_packf(e0, e1));
+                        pk[e] = pack_bf16x2(e0, e1) & keep;
+                        sumr = f2_add(sumr, f2_pack(pk[e] << 16, pk[e] & 0xffff0000u));
                     }
+                    l2 = keep ? f2_add(l2, sum) : l2;
+                    lr2 = f2_add(lr2, sumr);
                     tmem_st16(tS + 16 * c, pk);
                 }
             }
@@ -385,40 +470,67 @@ __global__ void __launch_bounds__((4 * NWG + 2) * 32, 1)
             if (lane == 0) mbar_arrive(&s.p_ready[buf]);
         }
         // -------------------------------------------------------------------- outputs
+        // Through shared memory (Q and K are no longer read: pv_done of the last tile follows every S), 64 columns
+        // at a time, so that a warp writes whole rows: 32 rows of 16-byte pieces straight from the lanes took
+        // 4 us at the end of every CTA.
         if (ok && n_tiles > 0) {
             ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[w], (n_tiles - 1) & 1, a.status, 0xc34));
             tc_fence_after();
         }
-        const int node = n0 + nl;
         if (ok) {
-            const int64_t orow = ((int64_t)b * a.T + node) * a.H_q + r * G + h;
-            const bool write = node < a.T, has = l > 0.f || l != l;  // a NaN sum stays NaN
-            const float inv = has ? 1.f / lr : 0.f;
-            const float lse = has ? (mref + log2f(l)) * 0.6931471805599453f : -INFINITY;
             const bool part = a.splits > 1;
-            if (write && part) a.lse_part[split * n_rows + orow] = lse;
-            if (write && !part && a.lse) a.lse[orow] = lse;
+            float l0, l1, r0, r1;
+            f2_unpack(l2, l0, l1);
+            f2_unpack(lr2, r0, r1);
+            const float l = l0 + l1;
+            const bool has = l > 0.f || l != l;  // a NaN sum stays NaN
+            const float inv = has ? 1.f / (r0 + r1) : 0.f;
+            const float lse = has ? (mref + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            // rows are consecutive heads of consecutive nodes: row i of the CTA is output row (node n0 + i / G, head)
+            auto out_row = [&](int i) { return ((int64_t)b * a.T + n0 + i / G) * a.H_q + r * G + i % G; };
+            const bool write = n0 + nl < a.T;
+            if (write && part) a.lse_part[split * n_rows + out_row(w * kRows + row)] = lse;
+            if (write && !part && a.lse) a.lse[out_row(w * kRows + row)] = lse;
             if (!part || n_tiles > 0) {
+                const bool half = !part && a.out_bf16;
+                uint8_t* stage = s.q[0] + warp * 8192;
+                const int pieces = half ? 8 : 16;  // 16-byte pieces of 64 columns
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
-                    uint32_t o[16];
-                    if (n_tiles > 0) {
-                        tmem_ld16(tO + 16 * c, o);
-                        tmem_ld_wait();
-                        reg_fence(o);
+                for (int c0 = 0; c0 < D; c0 += 64) {
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[16];
+                        if (n_tiles > 0) {
+                            tmem_ld16(tO + c0 + 16 * c, o);
+                            tmem_ld_wait();
+                            reg_fence(o);
+                        }
+                        float f[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) f[e] = has ? __uint_as_float(o[e]) * inv : 0.f;
+                        if (half) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                *reinterpret_cast<uint4*>(stage + lane * 128 + (((2 * c + e) ^ (lane & 7)) << 4)) =
+                                    make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
+                                               pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                *reinterpret_cast<float4*>(stage + lane * 256 + (((4 * c + e) ^ (lane & 7)) << 4)) =
+                                    make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                        }
                     }
-                    float f[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = has ? __uint_as_float(o[e]) * inv : 0.f;
-                    if (!write) continue;
-                    if (!part && a.out_bf16) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.out_bf16 + orow * D + 16 * c);
-                        dst[0] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-                        dst[1] = make_uint4(pack_bf16x2(f[8], f[9]), pack_bf16x2(f[10], f[11]), pack_bf16x2(f[12], f[13]), pack_bf16x2(f[14], f[15]));
-                    } else {
-                        float4* dst = reinterpret_cast<float4*>((part ? a.o_part + split * n_rows * D : a.out) + orow * D + 16 * c);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    __syncwarp();
+                    for (int i = lane; i < 32 * pieces; i += 32) {
+                        const int rr = i / pieces, pc = i % pieces, ri = w * kRows + (warp & 3) * 32 + rr;
+                        if (n0 + ri / G >= a.T) break;
+                        const uint4 val = *reinterpret_cast<const uint4*>(stage + rr * pieces * 16 + ((pc ^ (rr & 7)) << 4));
+                        uint8_t* dst = half ? reinterpret_cast<uint8_t*>(a.out_bf16 + out_row(ri) * D + c0)
+                                            : reinterpret_cast<uint8_t*>((part ? a.o_part + split * n_rows * D : a.out) +
+                                                                         out_row(ri) * D + c0);
+                        *reinterpret_cast<uint4*>(dst + pc * 16) = val;
                     }
                 }
             }
@@ -427,7 +539,7 @@ __global__ void __launch_bounds__((4 * NWG + 2) * 32, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 4 * NWG + 1) tmem_dealloc(tmem, 512);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
     pdl_trigger();
 }
 
@@ -514,7 +626,7 @@ cudaError_t run_tree_attn(const TreeArgs& a, const void* q, const void* k, const
         const size_t smem = std::max<size_t>(bytes + 1024, 120 * 1024);  // one CTA (512 TMEM columns) per SM
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        kern<<<grid, (4 * wg + 2) * 32, smem, st>>>(kp, vp, kd, vd, a, qb);
+        kern<<<grid, attn_threads(wg), smem, st>>>(kp, vp, kd, vd, a, qb);
         return cudaGetLastError();
     };
     auto pick = [&](auto d_c, auto bk_c) -> cudaError_t {
