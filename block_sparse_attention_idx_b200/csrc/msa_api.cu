@@ -184,6 +184,8 @@ TreeArgs tree_args(const msa_dims* d, const msa_pages* p, const msa_tree* t, Dev
     a.B = d->B; a.N = d->N; a.H_q = d->H_q; a.H_kv = d->H_kv; a.d = d->d; a.d_idx = d->d_idx;
     a.block_k = d->block_k; a.topk = d->topk; a.T = t->T;
     a.cols = page_cols(d);
+    while ((d->H_kv << a.lg_g) < d->H_q) ++a.lg_g;  // H_q / H_kv is a power of two
+    a.k1_inv = 65536 / (d->topk + 1) + 1;
     a.num_pages = p->num_pages;
     a.scale = eff_scale(d->scale, d->d);
     a.scale_idx = eff_scale(d->scale_idx, d->d_idx);

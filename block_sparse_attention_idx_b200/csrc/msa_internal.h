@@ -239,6 +239,8 @@ struct TreeArgs {
     int32_t* blocks_out;             // [B, T, H_kv, topk+1]
     float* margin_out;               // [B, T, H_kv] or null
     const int32_t* blocks;
+    int lg_g;                        // log2(H_q / H_kv)
+    int k1_inv;                      // floor(2^16 / (topk + 1)) + 1: e / (topk + 1) = e * k1_inv >> 16 for e < 3800
     int splits;                      // key splits of the attention
     float* o_part;                   // [splits, B, T, H_q, d] normalised partial outputs (splits > 1)
     float* lse_part;                 // [splits, B, T, H_q]

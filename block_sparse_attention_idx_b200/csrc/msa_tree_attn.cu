@@ -9,16 +9,17 @@
 // each entry with the set of nodes that chose it. Keys go in tiles of 128 (128 / block_k pages); the last
 // tile is the drafted tokens, masked to each node's ancestors in its selected blocks.
 //
-// Per tile and warpgroup: S = Q K^T (tcgen05, M = N = 128) in TMEM; a thread owns one row, takes the tile's
-// maximum, exponentials (base 2) and sums in fp32, writes P as bf16 over S; O += P V accumulates in TMEM.
-// The running maximum is only raised, and O rescaled, when a row's maximum grows by more than 2^8: exponents
-// stay far inside fp32 and bf16, and most tiles rescale nothing. O is normalised by the sum of the rounded P
-// that the product used, the LSE by the exact sum, as in the prefill and decode kernels. bf16 P costs at most
-// 2^-8 of each weight; the products and sums are fp32.
+// Per tile and 128 rows: S = Q K^T (tcgen05, M = N = 128) in TMEM; two threads share a row, 64 columns each: maximum,
+// exponentials (base 2) and sums in fp32, P as bf16 over S; O += P V accumulates in TMEM. The running maximum is
+// only raised, and O rescaled, when a row's maximum grows by more than 2^8: exponents stay far inside fp32 and bf16,
+// and most tiles rescale nothing. O and the LSE use the sum of the fp32 exponentials; P is rounded to bf16 for the
+// product, at most 2^-8 of each weight, and the products accumulate in fp32.
 //
 // NWG = 2 (more than 128 rows): two row tiles share K and V and alternate between the tensor cores and the
-// exponentials. NWG = 1: two S buffers, so that the next tile's S runs under this tile's softmax. Where the
-// CTAs do not fill the device the union is split over `splits` CTAs and merged by k_tree_combine.
+// exponentials. Where the CTAs do not fill the device the union is split over `splits` CTAs and merged by
+// k_tree_combine.
+#include <type_traits>
+
 #include "msa_tree.cuh"
 
 namespace msa {
@@ -31,7 +32,7 @@ constexpr int kWords = kTreeMaxBlocks / 32;
 
 template <int D, int NWG>
 struct TreeAttnSmem {
-    alignas(1024) uint8_t q[NWG][kRows * D * 2];  // at the end, with the start of k: the outputs on their way out
+    alignas(1024) uint8_t q[NWG][kRows * D * 2];  // with the start of k, at the end: outputs on their way out
     alignas(1024) uint8_t k[2][kTile * D * 2];
     alignas(1024) uint8_t v[2][kTile * D * 2];
     unsigned long long mask[kMaxEntries];   // nodes of the CTA that chose the entry
@@ -42,22 +43,23 @@ struct TreeAttnSmem {
     uint32_t late[64];                      // blocks >= len / block_k in a node's list
     uint32_t bits[kWords];
     int before[kWords];
-    // s_full and p_ready: one per S buffer. A warp whose rows are masked runs ahead of the others, by one tile at
-    // most, and must not arrive twice on one barrier for them.
+    float row_max[NWG][2][kRows];           // exchange between the two threads of a row
+    float row_sum[NWG][2][kRows];
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], pv_done[2], drain;
     int total;
     uint32_t tmem_base;
 };
 
-// Threads: the softmax warpgroups, then a TMA and an MMA warp. With NWG = 2 these two are part of a third
-// warpgroup (two of its warps only help in the prologue) that gives up registers: 384 threads start with 168
-// each (64512), 128 of them drop to 72 and 256 rise to 216 (9216 + 55296 = 64512), so that a row's 128 scores
-// stay in registers.
-constexpr int attn_threads(int nwg) { return nwg == 2 ? 384 : 192; }
-template <int N>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+// Threads: two softmax warpgroups per row tile, then a warpgroup with the TMA and the MMA warp (its other two warps
+// only help in the prologue): 640 threads of 96 registers with NWG = 2.
+constexpr int attn_threads(int nwg) { return (8 * nwg + 4) * 32; }
+
+// Three-input maximum that keeps a NaN.
+__device__ __forceinline__ float max3n(float a, float b, float c) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
 
 template <int D, int BK, int NWG>
 __global__ void __launch_bounds__(attn_threads(NWG), 1)
@@ -67,16 +69,17 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
     using Sm = TreeAttnSmem<D, NWG>;
     constexpr int TPT = kTile / BK;
     constexpr int NT = attn_threads(NWG);
-    constexpr int kTmaWarp = 4 * NWG, kMmaWarp = 4 * NWG + 1;
+    constexpr int kTmaWarp = 8 * NWG, kMmaWarp = 8 * NWG + 1;
     constexpr uint32_t kHalf = kTile * 128;  // bytes of a 64-column half of a 128-row tile
     constexpr uint32_t kTileBytes = kTile * D * 2;
-    constexpr int kColO = 256;
+    constexpr int kColO = 256;  // TMEM columns: S (then P) of row tile w at 128 w, O at 256 + 128 w
     constexpr int EPT = (kMaxEntries + NT - 1) / NT;  // list entries per thread
     extern __shared__ uint8_t tree_raw[];
     Sm& s = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(tree_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
-    const int G = a.H_q / a.H_kv, K1 = a.topk + 1;
-    const int per_cta = NWG * kRows / G;  // nodes
+    const int lg = a.lg_g, K1 = a.topk + 1;     // G = 2^lg heads per group
+    const int per_cta = (NWG * kRows) >> lg;  // nodes
+    auto list_of = [&](int e) { return (e * a.k1_inv) >> 16; };  // e / K1
     const int n_ct = (a.T + per_cta - 1) / per_cta;
     const int ct = blockIdx.x % n_ct, br = blockIdx.x / n_ct, r = br % a.H_kv, b = br / a.H_kv;
     const int split = blockIdx.y, n0 = ct * per_cta;
@@ -90,7 +93,8 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
 #pragma unroll
     for (int x = 0; x < EPT; ++x) {
         const int e = tid + x * NT;
-        id[x] = e < n_ent ? a.blocks[(((int64_t)b * a.T + n0 + e / K1) * a.H_kv + r) * K1 + e % K1] : -1;
+        const int nl = list_of(e);
+        id[x] = e < n_ent ? a.blocks[(((int64_t)b * a.T + n0 + nl) * a.H_kv + r) * K1 + e - nl * K1] : -1;
     }
     int p0 = -1, p1 = -1;
     if (warp == kTmaWarp) {
@@ -99,11 +103,11 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
     }
     const int len = tree_len(a, b), nodes = tree_nodes(a, b);
     for (int i = tid; i < NWG * kRows * (D / 8); i += NT) {
-        const int row = i / (D / 8), c = i % (D / 8), node = n0 + row / G, h = row % G;
+        const int row = i / (D / 8), c = i % (D / 8), node = n0 + (row >> lg), h = row & ((1 << lg) - 1);
         const uint32_t dst = smem_u32(s.q[0]) + (row / kRows) * (kRows * D * 2) + (c / 8) * kHalf +
                              swz(row % kRows, (c % 8) * 16, 128);
         const bool live = node < a.T;
-        cp_async_16_zfill(dst, live ? q + (((int64_t)b * a.T + node) * a.H_q + r * G + h) * D + c * 8 : q, live);
+        cp_async_16_zfill(dst, live ? q + (((int64_t)b * a.T + node) * a.H_q + (r << lg) + h) * D + c * 8 : q, live);
     }
     if (warp == kMmaWarp) {
         tmem_alloc(&s.tmem_base, 512);
@@ -119,7 +123,7 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
             mbar_init(&s.v_full[x], 1);
             mbar_init(&s.v_empty[x], 1);
             mbar_init(&s.s_full[x], 1);
-            mbar_init(&s.p_ready[x], 4);
+            mbar_init(&s.p_ready[x], 8);
             mbar_init(&s.pv_done[x], 1);
         }
         mbar_init(&s.drain, 1);
@@ -153,7 +157,7 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
     const int mine = max(0, min(per_cta, nodes - n0));  // nodes of this CTA that exist
 #pragma unroll
     for (int x = 0; x < EPT; ++x) {
-        const int e = tid + x * NT, nl = e / K1;
+        const int nl = list_of(tid + x * NT);
         pg[x] = 0;
         if (id[x] == -1 || nl >= mine) {
             id[x] = -1;
@@ -212,7 +216,7 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
         if (id[x] < 0) continue;
         const int c = id[x], at = s.before[c >> 5] + __popc(s.bits[c >> 5] & ((1u << (c & 31)) - 1u));
         if (at < e_lo || at >= e_hi) continue;
-        atomicOr(&s.mask[at - e_lo], 1ull << ((tid + x * NT) / K1));
+        atomicOr(&s.mask[at - e_lo], 1ull << list_of(tid + x * NT));
         s.page[at - e_lo] = pg[x];
     }
     // keys of the last page tile: the cache's last page, if chosen, holds len % block_k
@@ -228,7 +232,6 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
     const int n_tiles = t1 - t0;
 
     if (warp >= kTmaWarp) {
-    if constexpr (NWG == 2) regs_dec<72>();
     if (warp == kTmaWarp) {
         // -------------------------------------------------------------------- TMA producer
         const bool leader = elect_one();
@@ -276,23 +279,22 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
         const bool leader = elect_one();
         const uint64_t dq = umma_sdesc(smem_u32(s.q[0]), 16, 1024, 2), dk = umma_sdesc(smem_u32(s.k[0]), 16, 1024, 2);
         const uint64_t dv = umma_sdesc(smem_u32(s.v[0]), kHalf, 1024, 2);
+        constexpr uint32_t kIdescO = umma_idesc_bf16(kRows, D, false, true);
+        auto keys16 = [&](int j) { return (uint32_t)(tile_keys(t0 + j) + 15) / 16; };  // in the product's granularity
         auto issue_s = [&](int w, int j) {
-            const uint32_t nk = (uint32_t)(tile_keys(t0 + j) + 15) & ~15u;
-            const uint32_t idesc = umma_idesc_bf16(kRows, 0, false, false) | ((nk >> 3) << 17);
-            const int buf = NWG == 1 ? (j & 1) : w;
+            const uint32_t idesc = umma_idesc_bf16(kRows, 0, false, false) | (keys16(j) << 18);
             if (leader) {
                 const uint64_t qd = dq + w * (kTileBytes >> 4), kd = dk + (j & 1) * (kTileBytes >> 4);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint32_t off = ((ks / 4) * kHalf + (ks & 3) * 32) >> 4;
-                    umma_bf16(tmem + buf * kTile, qd + off, kd + off, idesc, ks > 0);
+                    umma_bf16(tmem + w * kTile, qd + off, kd + off, idesc, ks > 0);
                 }
-                umma_commit(&s.s_full[buf]);
+                umma_commit(&s.s_full[w]);
                 if (w == NWG - 1) umma_commit(&s.k_empty[j & 1]);
             }
             __syncwarp();
         };
-        constexpr uint32_t kIdescO = umma_idesc_bf16(kRows, D, false, true);
         bool ok = true;
         if (n_tiles > 0) {
             ok = mbar_wait(&s.k_full[0], 0, a.status, 0xc21);
@@ -303,235 +305,250 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
         }
         for (int j = 0; ok && j < n_tiles; ++j) {
             const bool more = j + 1 < n_tiles;
-            if (more) ok = mbar_wait(&s.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, a.status, 0xc22);
-            if (NWG == 1 && ok && more) {
-                tc_fence_after();
-                issue_s(0, j + 1);
-            }
-            ok = ok && mbar_wait(&s.v_full[j & 1], (j >> 1) & 1, a.status, 0xc23);
-            const int steps = (tile_keys(t0 + j) + 15) / 16;
+            const int steps = keys16(j);
+            ok = mbar_wait(&s.v_full[j & 1], (j >> 1) & 1, a.status, 0xc23);
+            if (ok && more) ok = mbar_wait(&s.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, a.status, 0xc22);
 #pragma unroll
             for (int w = 0; w < NWG; ++w) {
-                const int buf = NWG == 1 ? (j & 1) : w;
-                ok = ok && mbar_wait(&s.p_ready[buf], (NWG == 1 ? j >> 1 : j) & 1, a.status, 0xc24);
+                ok = ok && mbar_wait(&s.p_ready[w], j & 1, a.status, 0xc24);
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
-                    const uint32_t tP = tmem + buf * kTile, tO = tmem + kColO + w * kRows;
+                    const uint32_t tP = tmem + w * kTile, tO = tmem + kColO + w * kRows;
                     const uint64_t vd = dv + (j & 1) * (kTileBytes >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < kTile / 16; ++ks)
-                        if (ks < steps) umma_bf16_tmem_a(tO, tP + 8 * ks, vd + ((ks * 16 * 128) >> 4), kIdescO, j > 0 || ks > 0);
-                    umma_commit(&s.pv_done[w]);
+                    for (int ks = 0; ks < kTile / 16; ++ks)  // P of keys 64 .. 127 starts at column 64
+                        if (ks < steps)
+                            umma_bf16_tmem_a(tO, tP + (ks / 4) * 64 + (ks & 3) * 8, vd + ((ks * 16 * 128) >> 4), kIdescO,
+                                             j > 0 || ks > 0);
+                    if (!more) umma_commit(&s.pv_done[w]);
                     if (w == NWG - 1) umma_commit(&s.v_empty[j & 1]);
                 }
                 __syncwarp();
-                if (NWG == 2 && more) issue_s(w, j + 1);
+                if (more) issue_s(w, j + 1);
             }
         }
         if (leader) umma_commit(&s.drain);
         mbar_wait(&s.drain, 0, a.status, 0xc25);
     }
     } else {
-        if constexpr (NWG == 2) regs_inc<216>();
-        // -------------------------------------------------------------------- softmax: one row per thread
-        const int w = warp >> 2, row = (warp & 3) * 32 + lane;
-        const int nl = (w * kRows + row) / G;
+        // -------------------------------------------------------------------- softmax: two threads per row
+        // Thread (w, hf, row): columns 64 hf .. 64 hf + 63 of row tile w's S. Four warps per scheduler hide each
+        // other's latencies (one thread per row, 128 columns each, issued 0.34 instructions a cycle).
+        constexpr int CW = D / 2;  // output columns of a thread
+        const int w = warp >> 3, hf = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
+        const uint32_t pair_bar = 1 + w * 4 + (warp & 3);  // the two warps of these 32 rows
+        const int nl = (w * kRows + row) >> lg;
         const bool live = nl < mine;
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t tO = lane_addr + kColO + w * kRows;
+        const uint32_t tS = lane_addr + w * kTile + hf * 64, tO = lane_addr + kColO + w * kRows + hf * CW;
         const float sl2 = a.scale * 1.4426950408889634f;
         const uint64_t sl2x2 = f2_packf(sl2, sl2);
         const uint32_t* my_mask = reinterpret_cast<const uint32_t*>(s.mask) + ((nl >> 5) & 1);  // this row's word of an entry
         const uint32_t my_bit = live ? 1u << (nl & 31) : 0u;
         float mref = -INFINITY;
-        uint64_t l2 = f2_packf(0.f, 0.f), lr2 = l2;  // the row's sum and that of the rounded P, two halves each
+        uint64_t l2 = f2_packf(0.f, 0.f);  // the thread's part of the row's sum, two halves
         bool ok = true;
-        for (int j = 0; j < n_tiles; ++j) {
-            const int t = t0 + j, keys = tile_keys(t), buf = NWG == 1 ? (j & 1) : w;
+        for (int j = 0; ok && j < n_tiles; ++j) {
+            const int t = t0 + j, keys = tile_keys(t);
             const bool whole = t < page_tiles && keys == kTile;  // every column is a cached key
-            // chunks of 32 columns that this row sees, as all-ones or zero words; in a tile that is not whole the
-            // columns one by one
-            uint32_t see[4];
+            // this thread's two chunks of 32 columns: all-ones or zero words; in a tile that is not whole the columns
+            // one by one
+            uint32_t see[2];
             if (t < page_tiles) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int e = c / (BK / 32);
-                    see[c] = t * TPT + e < U && (my_mask[2 * (t * TPT + e - e_lo)] & my_bit) ? 0xffffffffu : 0u;
+                for (int c = 0; c < 2; ++c) {
+                    const int e = t * TPT + (2 * hf + c) / (BK / 32);
+                    see[c] = (TPT == 1 || e < U) && (my_mask[2 * (e - e_lo)] & my_bit) ? 0xffffffffu : 0u;
                     if (!whole) {
-                        const int left = keys - 32 * c;  // keys in this chunk
+                        const int left = keys - 64 * hf - 32 * c;  // keys in this chunk
                         see[c] &= left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
                     }
                 }
             } else {
-                const unsigned long long d = live ? s.draft[nl] : 0ull;
+                const unsigned long long d = live && hf == 0 ? s.draft[nl] : 0ull;
                 see[0] = (uint32_t)d;
                 see[1] = (uint32_t)(d >> 32);
-                see[2] = see[3] = 0u;
             }
             // rows of V behind the tile's last key, up to the product's depth, hold whatever the page or the
             // stage held before: zeros, so that P = 0 there gives 0 even against NaN
             const int pad = ((keys + 15) & ~15) - keys;
             if (w == 0 && pad) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&s.v_full[j & 1], (j >> 1) & 1, a.status, 0xc31));
-                for (int i = row; ok && i < pad * (D / 8); i += kRows) {
+                for (int i = hf * kRows + row; ok && i < pad * (D / 8); i += 2 * kRows) {
                     const int vr = keys + i / (D / 8), c = i % (D / 8);
                     *reinterpret_cast<uint4*>(s.v[j & 1] + (c / 8) * kHalf + swz(vr, (c % 8) * 16, 128)) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async();
             }
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&s.s_full[buf], (NWG == 1 ? j >> 1 : j) & 1, a.status, 0xc32));
-            if (!ok) break;
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&s.s_full[w], j & 1, a.status, 0xc32));
+            // (S of this tile was issued after the PV of the one before: O is not being written)
             tc_fence_after();
-            const uint32_t tS = lane_addr + buf * kTile;
-            if (!__any_sync(0xffffffffu, (see[0] | see[1] | see[2] | see[3]) != 0u)) {
-                uint32_t z[16];
+            const bool any = ok && __any_sync(0xffffffffu, (see[0] | see[1]) != 0u);
+            // S is read twice, 32 columns at a time: all 64 in registers spilled, and the reloads took longer than this
+            float mx = -INFINITY;
+            bool odd = false;  // a NaN or +inf among the scores
+            if (any) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) z[i] = 0u;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_st16(tS + 16 * c, z);
-            } else {
-                uint32_t x[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, x[c]);
-                tmem_ld_wait();
-                float mx = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    reg_fence(x[c]);
-                    float* f = reinterpret_cast<float*>(x[c]);
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t x[32];
+                    tmem_ld32(tS + 32 * c, x);
+                    tmem_ld_wait();
+                    reg_fence(x);
+                    float* f = reinterpret_cast<float*>(x);
                     if (!whole) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) f[e] = (see[c] >> e) & 1 ? f[e] : -INFINITY;
                     }
-                    float m0 = max3f(f[0], f[1], f[2]), m1 = max3f(f[3], f[4], f[5]);
+                    float m0 = max3n(f[0], f[1], f[2]), m1 = max3n(f[3], f[4], f[5]);
 #pragma unroll
                     for (int e = 6; e < 30; e += 4) {
-                        m0 = max3f(m0, f[e], f[e + 1]);
-                        m1 = max3f(m1, f[e + 2], f[e + 3]);
+                        m0 = max3n(m0, f[e], f[e + 1]);
+                        m1 = max3n(m1, f[e + 2], f[e + 3]);
                     }
-                    m0 = max3f(m0, m1, fmaxf(f[30], f[31]));
+                    m0 = max3n(m0, m1, max3n(f[30], f[31], f[31]));
+                    const bool strange = !(m0 < INFINITY);
+                    odd = odd || strange;
+                    // a NaN or infinite score that the row sees makes the row NaN
+                    if (strange && see[c]) l2 = f2_packf(NAN, NAN);
                     mx = see[c] ? fmaxf(mx, m0) : mx;
                 }
                 mx *= sl2;
-                if (j == 0) {
-                    mref = mx;
-                } else {
-                    const bool up = mx > mref + 8.f;
-                    if (__any_sync(0xffffffffu, up)) {
-                        ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[w], (j - 1) & 1, a.status, 0xc33));
-                        if (!ok) break;
-                        tc_fence_after();
-                        const float f = up ? fast_exp2(mref - mx) : 1.f;
-                        if (up) mref = mx;
-                        l2 = f2_mul(l2, f2_packf(f, f));
-                        lr2 = f2_mul(lr2, f2_packf(f, f));
+            }
+            // the running maximum, common to the row's two threads, is only touched when one of the 64 has to (or a
+            // wait ran out: the two warps leave together)
+            if (bar_red_or(pair_bar, 64, !ok || j == 0 || mx > mref + 8.f)) {
+                s.row_max[w][hf][row] = mx;
+                if (bar_red_or(pair_bar, 64, !ok)) {
+                    ok = false;
+                    break;
+                }
+                const float m2 = fmaxf(mx, s.row_max[w][hf ^ 1][row]);
+                const bool up = j == 0 || m2 > mref + 8.f;
+                if (j > 0) {
+                    const float f = up ? fast_exp2(mref - m2) : 1.f;
+                    l2 = f2_mul(l2, f2_packf(f, f));
 #pragma unroll
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t o[16];
-                            tmem_ld16(tO + 16 * c, o);
-                            tmem_ld_wait();
-                            reg_fence(o);
+                    for (int c = 0; c < CW / 16; ++c) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + 16 * c, o);
+                        tmem_ld_wait();
+                        reg_fence(o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st16(tO + 16 * c, o);
-                        }
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st16(tO + 16 * c, o);
                     }
                 }
+                if (up) mref = m2;
+            }
+            if (!any) {
+                uint32_t z[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) z[i] = 0u;
+                tmem_st16(tS, z);
+                tmem_st16(tS + 16, z);
+            } else {
                 const float base = mref == -INFINITY ? 0.f : mref;
-                const uint64_t nb2 = f2_packf(-base, -base);
+                // Whole tiles: a chunk that the row does not see gets base = +inf, so that every finite score gives
+                // exactly 0. Others, and tiles with a NaN or an infinite score (maybe of rows that do not see it): the
+                // unseen columns become -inf one by one.
+                auto weights = [&](auto plain_c) {
+                    constexpr bool kPlain = decltype(plain_c)::value;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    // a chunk that the row does not see in a whole tile: its P and its part of the sum are dropped
-                    const uint32_t keep = whole ? see[c] : 0xffffffffu;
-                    uint32_t pk[16];
-                    uint64_t sum = f2_packf(0.f, 0.f), sumr = sum;
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t x[32], pk[16];
+                        tmem_ld32(tS + 32 * c, x);
+                        tmem_ld_wait();
+                        reg_fence(x);
+                        if (!kPlain) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float z0, z1;
-                        f2_unpack(f2_fma(f2_pack(x[c][2 * e], x[c][2 * e + 1]), sl2x2, nb2), z0, z1);
-                        const float e0 = fast_exp2(z0), e1 = fast_exp2(z1);
-                        sum = f2_add(sum, f2_packf(e0, e1));
-                        pk[e] = pack_bf16x2(e0, e1) & keep;
-                        sumr = f2_add(sumr, f2_pack(pk[e] << 16, pk[e] & 0xffff0000u));
+                            for (int e = 0; e < 32; ++e) x[e] = (see[c] >> e) & 1 ? x[e] : 0xff800000u;
+                        }
+                        const float nb = kPlain && !see[c] ? -INFINITY : -base;
+                        const uint64_t nb2 = f2_packf(nb, nb);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float e0, e1;
+                            f2_unpack(f2_fma(f2_pack(x[2 * e], x[2 * e + 1]), sl2x2, nb2), e0, e1);
+                            e0 = fast_exp2(e0);
+                            e1 = fast_exp2(e1);
+                            l2 = f2_add(l2, f2_packf(e0, e1));
+                            pk[e] = pack_bf16x2(e0, e1);
+                        }
+                        tmem_st16(tS + 16 * c, pk);
                     }
-                    l2 = keep ? f2_add(l2, sum) : l2;
-                    lr2 = f2_add(lr2, sumr);
-                    tmem_st16(tS + 16 * c, pk);
-                }
+                };
+                if (whole && !__any_sync(0xffffffffu, odd)) weights(std::true_type{});
+                else weights(std::false_type{});
             }
             tmem_st_wait();
-            // every phase of pv_done is waited for in turn (a parity wait cannot tell a phase from the next but
-            // one): PV of the previous tile ran under this tile's exponentials, so this costs nothing
-            if (j > 0) ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[w], (j - 1) & 1, a.status, 0xc35));
-            if (!ok) break;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.p_ready[buf]);
+            if (lane == 0) mbar_arrive(&s.p_ready[w]);
         }
         // -------------------------------------------------------------------- outputs
-        // Through shared memory (Q and K are no longer read: pv_done of the last tile follows every S), 64 columns
-        // at a time, so that a warp writes whole rows: 32 rows of 16-byte pieces straight from the lanes took
-        // 4 us at the end of every CTA.
+        // Through shared memory (Q and K are no longer read: the last S of both row tiles was issued before a last
+        // PV), so that a warp writes whole rows: 32 rows of 16-byte pieces straight from the lanes took 4 us at the
+        // end of every CTA.
         if (ok && n_tiles > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[w], (n_tiles - 1) & 1, a.status, 0xc34));
+            ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[w], 0, a.status, 0xc34));
             tc_fence_after();
         }
+        float l0, l1;
+        f2_unpack(l2, l0, l1);
+        s.row_sum[w][hf][row] = l0 + l1;
+        bar_sync_named(pair_bar, 64);
         if (ok) {
+            const float l = s.row_sum[w][0][row] + s.row_sum[w][1][row];
             const bool part = a.splits > 1;
-            float l0, l1, r0, r1;
-            f2_unpack(l2, l0, l1);
-            f2_unpack(lr2, r0, r1);
-            const float l = l0 + l1;
             const bool has = l > 0.f || l != l;  // a NaN sum stays NaN
-            const float inv = has ? 1.f / (r0 + r1) : 0.f;
+            const float inv = has ? 1.f / l : 0.f;
             const float lse = has ? (mref + log2f(l)) * 0.6931471805599453f : -INFINITY;
-            // rows are consecutive heads of consecutive nodes: row i of the CTA is output row (node n0 + i / G, head)
-            auto out_row = [&](int i) { return ((int64_t)b * a.T + n0 + i / G) * a.H_q + r * G + i % G; };
-            const bool write = n0 + nl < a.T;
+            // rows are consecutive heads of consecutive nodes: row i of the CTA is head i % G of node n0 + i / G
+            auto out_row = [&](int i) {
+                return ((int64_t)b * a.T + n0 + (i >> lg)) * a.H_q + (r << lg) + (i & ((1 << lg) - 1));
+            };
+            const bool write = hf == 0 && n0 + nl < a.T;
             if (write && part) a.lse_part[split * n_rows + out_row(w * kRows + row)] = lse;
             if (write && !part && a.lse) a.lse[out_row(w * kRows + row)] = lse;
             if (!part || n_tiles > 0) {
                 const bool half = !part && a.out_bf16;
-                uint8_t* stage = s.q[0] + warp * 8192;
-                const int pieces = half ? 8 : 16;  // 16-byte pieces of 64 columns
+                uint8_t* stage = s.q[0] + warp * (32 * CW * 4);
+                const int lp = (half ? 1 : 2) + (CW == 64 ? 2 : 1), pieces = 1 << lp;  // 16-byte pieces of a row
+                const int sw = pieces - 1 < 7 ? pieces - 1 : 7;
 #pragma unroll
-                for (int c0 = 0; c0 < D; c0 += 64) {
-                    __syncwarp();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[16];
-                        if (n_tiles > 0) {
-                            tmem_ld16(tO + c0 + 16 * c, o);
-                            tmem_ld_wait();
-                            reg_fence(o);
-                        }
-                        float f[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) f[e] = has ? __uint_as_float(o[e]) * inv : 0.f;
-                        if (half) {
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                *reinterpret_cast<uint4*>(stage + lane * 128 + (((2 * c + e) ^ (lane & 7)) << 4)) =
-                                    make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
-                                               pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                *reinterpret_cast<float4*>(stage + lane * 256 + (((4 * c + e) ^ (lane & 7)) << 4)) =
-                                    make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-                        }
+                for (int c = 0; c < CW / 16; ++c) {
+                    uint32_t o[16];
+                    if (n_tiles > 0) {
+                        tmem_ld16(tO + 16 * c, o);
+                        tmem_ld_wait();
+                        reg_fence(o);
                     }
-                    __syncwarp();
-                    for (int i = lane; i < 32 * pieces; i += 32) {
-                        const int rr = i / pieces, pc = i % pieces, ri = w * kRows + (warp & 3) * 32 + rr;
-                        if (n0 + ri / G >= a.T) break;
-                        const uint4 val = *reinterpret_cast<const uint4*>(stage + rr * pieces * 16 + ((pc ^ (rr & 7)) << 4));
-                        uint8_t* dst = half ? reinterpret_cast<uint8_t*>(a.out_bf16 + out_row(ri) * D + c0)
-                                            : reinterpret_cast<uint8_t*>((part ? a.o_part + split * n_rows * D : a.out) +
-                                                                         out_row(ri) * D + c0);
-                        *reinterpret_cast<uint4*>(dst + pc * 16) = val;
+                    float f[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) f[e] = has ? __uint_as_float(o[e]) * inv : 0.f;
+                    if (half) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<uint4*>(stage + (lane << (lp + 4)) + (((2 * c + e) ^ (lane & sw)) << 4)) =
+                                make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
+                                           pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<float4*>(stage + (lane << (lp + 4)) + (((4 * c + e) ^ (lane & sw)) << 4)) =
+                                make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
                     }
+                }
+                __syncwarp();
+                for (int i = lane; i < 32 << lp; i += 32) {
+                    const int rr = i >> lp, pc = i & (pieces - 1), ri = w * kRows + (warp & 3) * 32 + rr;
+                    if (n0 + (ri >> lg) >= a.T) break;
+                    const uint4 val = *reinterpret_cast<const uint4*>(stage + (rr << (lp + 4)) + ((pc ^ (rr & sw)) << 4));
+                    uint8_t* dst = half ? reinterpret_cast<uint8_t*>(a.out_bf16 + out_row(ri) * D + hf * CW)
+                                        : reinterpret_cast<uint8_t*>((part ? a.o_part + split * n_rows * D : a.out) +
+                                                                     out_row(ri) * D + hf * CW);
+                    *reinterpret_cast<uint4*>(dst + pc * 16) = val;
                 }
             }
         }

@@ -56,11 +56,11 @@ def node_decode(dims: Dims, q, q_idx, k, v, k_idx):
 
 def attend(dims: Dims, q, k, v, blocks):
     """One node's attention over its virtual sequence k, v [L, H_kv, d] for block lists blocks [H_kv, *]: (out
-    [H_q, d], lse [H_q], dev [H_q, d]), dev the weighted mean of |v - out|, the scale of an error in the weights."""
+    [H_q, d], lse [H_q], mag [H_q, d]), mag the weighted mean of |v|, the scale of an error in the weights."""
     L, G = k.shape[0], dims.H_q // dims.H_kv
     scale = dims.scale if dims.scale > 0 else 1.0 / math.sqrt(dims.d)
     qd, kd, vd = (t.double().cpu().numpy() for t in (q, k, v))
-    out, dev = np.zeros((dims.H_q, dims.d)), np.zeros((dims.H_q, dims.d))
+    out, mag = np.zeros((dims.H_q, dims.d)), np.zeros((dims.H_q, dims.d))
     lse = np.full(dims.H_q, -np.inf)
     for r in range(dims.H_kv):
         ids = sorted({int(c) for c in blocks[r] if c >= 0})
@@ -74,5 +74,5 @@ def attend(dims: Dims, q, k, v, blocks):
             lse[h] = m + math.log(w.sum())
             w /= w.sum()
             out[h] = w @ vd[J, r]
-            dev[h] = w @ np.abs(vd[J, r] - out[h])
-    return out, lse, dev
+            mag[h] = w @ np.abs(vd[J, r])
+    return out, lse, mag

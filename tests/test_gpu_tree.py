@@ -4,10 +4,13 @@ step on the node's virtual sequence (the cached tokens, its ancestors and itself
 Index vectors lie on a grid of 1/16 with magnitude up to 4: every product and sum of a score is exact in fp32
 in any order, so that block lists (ties included) have to be equal.
 
-Attention tolerance. P enters the product as bf16 (each weight off by at most 2^-8 of itself) and the output is
-normalised by the sum of the same rounded weights: |error| <= 2^-8 / (1 - 2^-8) sum_j w_j |v_j - o|. The logits
-(fp32 accumulation over d <= 128 products, |q.k| scale < 16) and the base-2 exponential are good to 3e-5
-relative, in the weights again. A bf16 output adds half a step, 2^-8 of the value. LSE: 3e-5."""
+Attention tolerance. The product takes p_j as bf16, p_j (1 + e_j) with |e_j| <= 2^-8, and the output is normalised
+by the sum of the unrounded p_j, as the prefill kernel's is: with w_j = p_j / sum p, the output is
+sum_j w_j (1 + e_j) v_j, so that |error| <= 2^-8 sum_j w_j |v_j|. (An earlier kernel normalised by the rounded
+weights' sum, error sum_j w_j e_j (v_j - o) / (1 + ...), and was tested against that smaller bound; the unrounded
+sum saves a third of the instructions of a weight.) The logits (fp32 accumulation over d <= 128 products,
+|q.k| scale < 16) and the base-2 exponential are good to 3e-5 relative, in the weights again. A bf16 output adds
+half a step, 2^-8 of the value. LSE: 3e-5."""
 import numpy as np
 import pytest
 import torch
@@ -114,8 +117,8 @@ class Case:
                     assert (got[b, n] == 0).all() and np.isneginf(glse[b, n]).all()
                     continue
                 K, V, _ = self.virtual(b, n)
-                o, l, dev = otree.attend(self.od, self.q[b, n].cpu(), K, V, lists[b, n])
-                tol = (2.0 ** -8 / (1 - 2.0 ** -8) + 3e-5) * dev * (1 + half) + half * np.abs(o) + 1e-6
+                o, l, mag = otree.attend(self.od, self.q[b, n].cpu(), K, V, lists[b, n])
+                tol = (2.0 ** -8 + 3e-5) * mag * (1 + half) + half * np.abs(o) + 1e-6
                 assert (np.abs(got[b, n] - o) <= tol).all(), (b, n, np.abs(got[b, n] - o).max())
                 f = np.isfinite(l)
                 assert np.array_equal(f, np.isfinite(glse[b, n]))
@@ -215,9 +218,9 @@ def test_a_growing_maximum_rescales_what_was_summed():
         x[~torch.isnan(x)] *= 2.0 ** (p / 2)
     out, lse = c.attend(blocks, want_lse=True)
     K, V, _ = c.virtual(0, 0)
-    o, l, dev = otree.attend(c.od, c.q[0, 0].cpu(), K, V, blocks[0, 0].cpu().numpy())
+    o, l, mag = otree.attend(c.od, c.q[0, 0].cpu(), K, V, blocks[0, 0].cpu().numpy())
     # logits reach |60|: fp32 logits to 60 * 128 * 2^-24, weights to that relative
-    assert (np.abs(out[0, 0].double().cpu().numpy() - o) <= (2.0 ** -8 * 1.01 + 5e-4) * dev + 1e-5).all()
+    assert (np.abs(out[0, 0].double().cpu().numpy() - o) <= (2.0 ** -8 + 5e-4) * mag + 1e-5).all()
     assert np.abs(lse[0, 0].double().cpu().numpy() - l).max() < 5e-4
 
 
