@@ -245,14 +245,12 @@ msa_status rope_call(const msa_rope_seg* seg, int nseg, int64_t tokens, const in
         RopeSeg& o = a.seg[i];
         o.x = g.x; o.y = g.y; o.x_stride = g.x_stride; o.y_stride = g.y_stride; o.inv_freq = g.inv_freq;
         o.heads = g.heads; o.dim = g.dim; o.rot = g.rot; o.amp = g.amp;
-        o.vec = 8;
-        while (g.rot / 2 % o.vec != 0) o.vec /= 2;
     }
     a.nseg = nseg;
     a.tokens = tokens;
     a.positions = positions;
     a.back = back;
-    return cuda_status(run_rope(a, interleaved != 0, xs == 4, ys == 4, num_sms(), reinterpret_cast<cudaStream_t>(stream_)));
+    return cuda_status(run_rope(a, interleaved != 0, xs == 4, ys == 4, reinterpret_cast<cudaStream_t>(stream_)));
 }
 
 struct Carver {

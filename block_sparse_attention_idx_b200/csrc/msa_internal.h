@@ -190,8 +190,7 @@ struct RopeSeg {
     const double* inv_freq;  // [rot / 2]
     int heads, dim, rot;
     float amp;
-    int vec;                 // pairs per lane: the largest of 8, 4, 2, 1 that divides rot / 2
-    int heads_per_unit;      // set by run_rope
+    int tab, lg;             // set by run_rope: its table of cosines, log2 of its chunks per head
 };
 struct RopeArgs {
     RopeSeg seg[kRopeSegs];
@@ -199,10 +198,11 @@ struct RopeArgs {
     int64_t tokens;
     const int32_t* positions;  // [tokens], or null: position = token
     int back;                  // rotate by -angle
-    int units;                 // warps per token, set by run_rope
-    int unit0[kRopeSegs];      // first of a segment's units
+    // set by run_rope
+    int task0[kRopeSegs + 1];  // first of a segment's tasks (chunks of its heads) of a token
+    int ntab, tab_seg[kRopeSegs], tab0[kRopeSegs + 1];  // distinct tables: a segment that has it, first entry
 };
-cudaError_t run_rope(RopeArgs a, bool interleaved, bool x32, bool y32, int num_sms, cudaStream_t st);
+cudaError_t run_rope(RopeArgs a, bool interleaved, bool x32, bool y32, cudaStream_t st);
 
 // ---------------------------------------------------------------- paged caches (msa_pages.cu)
 struct AppendArgs {
