@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -216,8 +217,15 @@ def _stream(stream, dev: torch.device):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _raw_stream(stream, dev: torch.device):
+    """_stream for the short calls: the current stream's handle without a Stream object."""
+    if stream is None and dev.index == torch.cuda.current_device():
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    return _stream(stream, dev)
+
+
 def _need(t: torch.Tensor, name: str, shape, dtype, device):
-    if t.is_cuda and t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.device == device:
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda and t.get_device() == device.index:
         return
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor (the library takes device pointers), got {t.device}")
@@ -428,46 +436,50 @@ def _rope(fn: str, xs, freqs, positions, interleaved, outs, out_dtype, stream):
         out_dtype = dtype
     if dtype not in _ROPE_TYPES or out_dtype not in _ROPE_TYPES:
         raise ValueError(f"tensors must be torch.bfloat16 or torch.float32, got {dtype} -> {out_dtype}")
-    seg, made, tokens, seen = [], [], None, None
+    seg, made, tokens, seen, idx = b"", [], None, None, xs[0].get_device()
     for i, (x, (f, amp)) in enumerate(zip(xs, freqs)):
         if not x.is_cuda:
             raise ValueError(f"xs[{i}] must be a CUDA tensor (the library takes device pointers), got {x.device}")
-        if x.device != dev or x.dtype is not dtype:
+        if x.get_device() != idx or x.dtype is not dtype:
             raise ValueError(f"xs[{i}]: expected {dtype} on {dev}, got {x.dtype} on {x.device}")
-        n, heads, dim, sx = _token_rows(x, f"xs[{i}]")
-        if tokens is None:
+        n, heads, dim, sx = _token_rows(x, f"xs[{i}]" if i else "xs[0]")
+        if n != tokens:
+            if tokens is not None:
+                raise ValueError(f"xs[{i}] has {n} tokens, xs[0] has {tokens}")
             tokens = n
-        elif n != tokens:
-            raise ValueError(f"xs[{i}] has {n} tokens, xs[0] has {tokens}")
         if given:
             y = outs[i]
-            if y.device != dev or y.dtype is not out_dtype:
+            if y.get_device() != idx or y.dtype is not out_dtype:
                 raise ValueError(f"outs[{i}]: expected {out_dtype} on {dev}, got {y.dtype} on {y.device}")
             if x.shape != y.shape:
                 raise ValueError(f"outs[{i}]: expected shape {tuple(x.shape)}, got {tuple(y.shape)}")
             sy = _token_rows(y, f"outs[{i}]")[3]
         else:
-            if stream is None:
-                y = x.new_empty(x.shape, dtype=out_dtype)
-            else:
+            if stream is not None:
                 with torch.cuda.stream(stream):
                     y = x.new_empty(x.shape, dtype=out_dtype)
+            elif out_dtype is dtype and sx == heads * dim:
+                y = torch.empty_like(x)
+            else:
+                y = x.new_empty(x.shape, dtype=out_dtype)
             sy = heads * dim
         made.append(y)
         if f is not seen:
             if f.dim() != 1:
                 raise ValueError("inv_freq must be fp64 [rot / 2]")
             _need(f, "inv_freq", f.shape, torch.float64, dev)
-            seen = f
-        seg.append(_ROPE_SEG.pack(x.data_ptr(), y.data_ptr(), sx, sy, f.data_ptr(), heads, dim, 2 * f.numel(), amp))
+            seen, at, rot = f, f.data_ptr(), 2 * f.numel()
+        seg += _ROPE_SEG.pack(x.data_ptr(), y.data_ptr(), sx, sy, at, heads, dim, rot, amp)
     if positions is not None:
         _need(positions, "positions", positions.shape, torch.int32, dev)
         if positions.numel() != tokens:
             raise ValueError(f"positions: expected {tokens} values, got {positions.numel()}")
-    st = _stream(stream, dev)
+    st = _raw_stream(stream, dev)
     if tokens:
-        _check(fn, getattr(lib(), fn)(b"".join(seg), len(xs), tokens, _p(positions), int(interleaved), _ROPE_TYPES[dtype],
-                                      _ROPE_TYPES[out_dtype], st))
+        code = getattr(_lib or lib(), fn)(seg, len(xs), tokens, positions.data_ptr() if positions is not None else None,
+                                          int(interleaved), _ROPE_TYPES[dtype], _ROPE_TYPES[out_dtype], st)
+        if code:
+            _check(fn, code)
     return made
 
 
@@ -524,11 +536,13 @@ def msa_cache_append(dims: MsaDims, pages: MsaPages, k, v, k_idx, k_pool, v_pool
         _need(rows, "rows", (dims.B, T_new), torch.int32, dev)
     n = _pools(dims, (k_pool, v_pool, k_idx_pool), ("k_pool", "v_pool", "k_idx_pool"), dev)
     pg = _pages(dims, pages, n, dev)
-    wp, wn = _status_ws(ws, dev)
-    _check("msa_cache_append",
-           lib().msa_cache_append(ctypes.byref(dims.c()), ctypes.byref(pg), T, _p(k), _p(v), _p(k_idx), T_new,
-                                  _p(n_new), _p(rows), _p(k_pool), _p(v_pool), _p(k_idx_pool), wp, wn,
-                                  _stream(stream, dev)))
+    wp, wn = (None, 0) if ws is None else _status_ws(ws, dev)
+    code = (_lib or lib()).msa_cache_append(
+        ctypes.byref(dims.c()), ctypes.byref(pg), T, k.data_ptr(), v.data_ptr(), k_idx.data_ptr(), T_new, n_new.data_ptr(),
+        None if rows is None else rows.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), k_idx_pool.data_ptr(), wp, wn,
+        _raw_stream(stream, dev))
+    if code:
+        _check("msa_cache_append", code)
 
 
 def msa_cache_copy_pages(dims: MsaDims, src, dst, k_pool, v_pool, k_idx_pool, ws=None, stream=None):
@@ -551,11 +565,12 @@ def msa_cache_copy_pages(dims: MsaDims, src, dst, k_pool, v_pool, k_idx_pool, ws
         raise ValueError("src and dst must both be tensors or both sequences")
     _need(src, "src", (src.numel(),), torch.int32, dev)
     _need(dst, "dst", (src.numel(),), torch.int32, dev)
-    wp, wn = _status_ws(ws, dev)
-    st = _stream(stream, dev)
-    _check("msa_cache_copy_pages",
-           lib().msa_cache_copy_pages(ctypes.byref(dims.c()), n_pages, src.numel(), _p(src) if src.numel() else None,
-                                      _p(dst) if src.numel() else None, _p(k_pool), _p(v_pool), _p(k_idx_pool), wp, wn, st))
+    wp, wn = (None, 0) if ws is None else _status_ws(ws, dev)
+    code = (_lib or lib()).msa_cache_copy_pages(
+        ctypes.byref(dims.c()), n_pages, src.numel(), src.data_ptr() or None, dst.data_ptr() or None, k_pool.data_ptr(),
+        v_pool.data_ptr(), k_idx_pool.data_ptr(), wp, wn, _raw_stream(stream, dev))
+    if code:
+        _check("msa_cache_copy_pages", code)
 
 
 def msa_tree_workspace_size(op: int, dims: MsaDims, T: int) -> int:
@@ -569,6 +584,12 @@ def tree_workspace(op: int, dims: MsaDims, T: int, device) -> torch.Tensor:
     return torch.empty((max(msa_tree_workspace_size(op, dims, T), 256),), dtype=torch.uint8, device=device)
 
 
+@functools.lru_cache(maxsize=256)
+def _tree_ws_size(op, B, N, H_q, H_kv, d, d_idx, block_k, topk, T, device) -> int:
+    """msa_tree_workspace_size for sizes seen before on a device (it depends on the device's SM count)."""
+    return max(256, msa_tree_workspace_size(op, MsaDims(B, N, H_q, H_kv, d, d_idx, block_k, topk), T))
+
+
 def _tree(dims: MsaDims, tree: MsaTree, dev):
     T = tree.parents.shape[1] if tree.parents.dim() == 2 else 0
     _need(tree.parents, "parents", (dims.B, T), torch.int32, dev)
@@ -576,12 +597,13 @@ def _tree(dims: MsaDims, tree: MsaTree, dev):
     return T, _Tree(tree.parents.data_ptr(), tree.n_nodes.data_ptr(), T)
 
 
-def _tree_ws(ws, op: int, dims: MsaDims, T: int, dev, stream) -> torch.Tensor:
+def _tree_ws(ws, op: int, dims: MsaDims, T: int, like: torch.Tensor) -> torch.Tensor:
+    """The caller's workspace, checked, or a new one next to `like`, on the current stream."""
     if ws is None:
-        with _on(stream):
-            return tree_workspace(op, dims, T, dev)
-    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != dev:
-        raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
+        n = _tree_ws_size(op, dims.B, dims.N, dims.H_q, dims.H_kv, dims.d, dims.d_idx, dims.block_k, dims.topk, T, like.get_device())
+        return like.new_empty(n, dtype=torch.uint8)
+    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != like.device:
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {like.device}")
     return ws
 
 
@@ -595,13 +617,15 @@ def msa_tree_index_topk(dims: MsaDims, pages: MsaPages, tree: MsaTree, q_idx, k_
     _need(q_idx, "q_idx", (dims.B, T, dims.H_kv, dims.d_idx), torch.bfloat16, dev)
     _need(k_idx, "k_idx", (dims.B, T, dims.d_idx), torch.bfloat16, dev)
     pg = _pages(dims, pages, _pools(dims, (k_idx_pool,), ("k_idx_pool",), dev), dev)
-    ws = _tree_ws(ws, MSA_OP_TREE_INDEX_TOPK, dims, T, dev, stream)
     with _on(stream):
+        ws = _tree_ws(ws, MSA_OP_TREE_INDEX_TOPK, dims, T, q_idx)
         blocks = q_idx.new_empty((dims.B, T, dims.H_kv, dims.topk + 1), dtype=torch.int32)
         margin = q_idx.new_empty((dims.B, T, dims.H_kv), dtype=torch.float32) if want_margin else None
-    _check("msa_tree_index_topk",
-           lib().msa_tree_index_topk(ctypes.byref(dims.c()), ctypes.byref(pg), ctypes.byref(tr), _p(q_idx), _p(k_idx),
-                                     _p(k_idx_pool), _p(blocks), _p(margin), _p(ws), ws.numel(), _stream(stream, dev)))
+    code = (_lib or lib()).msa_tree_index_topk(
+        ctypes.byref(dims.c()), ctypes.byref(pg), ctypes.byref(tr), q_idx.data_ptr(), k_idx.data_ptr(), k_idx_pool.data_ptr(),
+        blocks.data_ptr(), None if margin is None else margin.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+    if code:
+        _check("msa_tree_index_topk", code)
     return (blocks, margin) if want_margin else blocks
 
 
@@ -619,16 +643,21 @@ def msa_tree_sparse_attn(dims: MsaDims, pages: MsaPages, tree: MsaTree, q, k, v,
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"out_dtype must be torch.float32 or torch.bfloat16, not {out_dtype}")
     pg = _pages(dims, pages, _pools(dims, (k_pool, v_pool), ("k_pool", "v_pool"), dev), dev)
-    ws = _tree_ws(ws, MSA_OP_TREE_ATTN, dims, T, dev, stream)
+    given = out is not None
     with _on(stream):
-        if out is None:
-            out = q.new_empty(q.shape, dtype=out_dtype)
+        ws = _tree_ws(ws, MSA_OP_TREE_ATTN, dims, T, q)
+        if not given:
+            out = torch.empty_like(q) if out_dtype is torch.bfloat16 else q.new_empty(q.shape, dtype=out_dtype)
         lse = q.new_empty((dims.B, T, dims.H_q), dtype=torch.float32) if want_lse else None
-    _need(out, "out", tuple(q.shape), out_dtype, dev)
-    fn = "msa_tree_sparse_attn" if out_dtype == torch.float32 else "msa_tree_sparse_attn_bf16"
-    _check(fn, getattr(lib(), fn)(ctypes.byref(dims.c()), ctypes.byref(pg), ctypes.byref(tr), _p(q), _p(k), _p(v),
-                                  _p(k_pool), _p(v_pool), _p(blocks), _p(out), _p(lse), _p(ws), ws.numel(),
-                                  _stream(stream, dev)))
+    if given:
+        _need(out, "out", tuple(q.shape), out_dtype, dev)
+    fn = "msa_tree_sparse_attn" if out_dtype is torch.float32 else "msa_tree_sparse_attn_bf16"
+    code = getattr(_lib or lib(), fn)(
+        ctypes.byref(dims.c()), ctypes.byref(pg), ctypes.byref(tr), q.data_ptr(), k.data_ptr(), v.data_ptr(), k_pool.data_ptr(),
+        v_pool.data_ptr(), blocks.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
+        _raw_stream(stream, dev))
+    if code:
+        _check(fn, code)
     return out, lse
 
 
