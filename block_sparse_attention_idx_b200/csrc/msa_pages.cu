@@ -9,46 +9,43 @@ namespace msa {
 
 namespace {
 
-// One warp per appended token: slot cache_len[b] + i gets row rows[b, i] (or i) of the new K, V and K_idx.
-// A token is 2 H_kv d + d_idx elements (2.1 KB at H_kv = 4, d = 128): each lane issues all of its 16-byte
-// loads of a tensor before the stores.
+// One warp per appended token: slot cache_len[b] + i gets row rows[b, i] (or i) of the new K, V and K_idx. A token is
+// 2 H_kv d + d_idx elements (2.1 KB at H_kv = 4, d = 128). Its loads are issued before its slot is known: they need the
+// row only, and the chain length -> page -> store is as long as they are.
 __global__ void __launch_bounds__(256) k_cache_append(const __grid_constant__ AppendArgs a) {
     const int lane = threadIdx.x & 31;
     const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int b = (int)(w / a.T_new), i = (int)(w - (int64_t)b * a.T_new);
     if (b >= a.B) return;
+    const int row = a.rows ? a.rows[(int64_t)b * a.T_new + i] : i;
     const int n = a.n_new[b], len = a.cache_len[b];
+    const bool row_ok = (unsigned)row < (unsigned)a.T;
+    const int64_t src = (int64_t)b * a.T + (row_ok ? row : 0);
+    uint4 k[4], v[4], ki;  // H_kv d <= 1024 elements: up to 4 vectors a lane
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+        if (lane + 32 * x < a.kv_vec) {
+            k[x] = a.k[src * a.kv_vec + lane + 32 * x];
+            v[x] = a.v[src * a.kv_vec + lane + 32 * x];
+        }
+    if (lane < a.idx_vec) ki = a.k_idx[src * a.idx_vec + lane];
     const bool bad_n = n < 0 || n > a.T_new || len < 0 || (n > 0 && len > a.N - n);
     if (bad_n && i == 0 && lane == 0 && a.status) raise_flag(a.status, MSA_DEV_BAD_BLOCK, 0xa01);
     if (i >= n || len < 0 || len > a.N - 1 - i) return;
     const int slot = len + i;
     const int page = a.page_table[(int64_t)b * a.cols + slot / a.block_k];
-    const int row = a.rows ? a.rows[(int64_t)b * a.T_new + i] : i;
-    if ((unsigned)page >= (unsigned)a.num_pages || (unsigned)row >= (unsigned)a.T) {
+    if ((unsigned)page >= (unsigned)a.num_pages || !row_ok) {
         if (lane == 0 && a.status) raise_flag(a.status, MSA_DEV_BAD_BLOCK, 0xa02);
         return;
     }
-    const int64_t src = (int64_t)b * a.T + row, dst = (int64_t)page * a.block_k + slot % a.block_k;
-    const uint4* k = a.k + src * a.kv_vec;
-    const uint4* v = a.v + src * a.kv_vec;
-    uint4* kp = a.k_pool + dst * a.kv_vec;
-    uint4* vp = a.v_pool + dst * a.kv_vec;
-    for (int x = lane; x < a.kv_vec; x += 64) {
-        const bool two = x + 32 < a.kv_vec;
-        const uint4 k0 = k[x], v0 = v[x];
-        uint4 k1, v1;
-        if (two) {
-            k1 = k[x + 32];
-            v1 = v[x + 32];
+    const int64_t dst = (int64_t)page * a.block_k + slot % a.block_k;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+        if (lane + 32 * x < a.kv_vec) {
+            a.k_pool[dst * a.kv_vec + lane + 32 * x] = k[x];
+            a.v_pool[dst * a.kv_vec + lane + 32 * x] = v[x];
         }
-        kp[x] = k0;
-        vp[x] = v0;
-        if (two) {
-            kp[x + 32] = k1;
-            vp[x + 32] = v1;
-        }
-    }
-    if (lane < a.idx_vec) a.k_idx_pool[dst * a.idx_vec + lane] = a.k_idx[src * a.idx_vec + lane];
+    if (lane < a.idx_vec) a.k_idx_pool[dst * a.idx_vec + lane] = ki;
 }
 
 // One CTA per 16 KB piece of a copied page (K pieces, then V, then K_idx): 256 threads with four 16-byte

@@ -315,23 +315,23 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
     return __uint_as_float((o & 0x80000000u) ? (o ^ 0x80000000u) : ~o);
 }
 
-// WPR warps rank one (node, group) row. The (k+1)-th largest of a warp's 32 lane maxima bounds its (k+1)-th
-// largest candidate from below, so only the candidates at or above that bound, about 1.3 (k+1) of them and
-// never more than k+1 lanes' worth, go to a list in shared memory, where each is ranked by counting. One
-// pass over the maxima held in registers, no histogram, no sort.
+// WPR warps rank one (node, group) row, PL candidates a lane. The (k+1)-th largest of a warp's 32 lane maxima bounds
+// its (k+1)-th largest candidate from below, so only the candidates at or above that bound, about 1.3 (k+1) of them
+// and never more than k+1 lanes' worth, go to a list in shared memory, where each is ranked by counting. One pass
+// over the maxima held in registers, no histogram, no sort. The list's worst case sizes the shared memory: with
+// 64 candidates a lane for every row count, 2048 rows of 391 blocks took 17 us at 6 CTAs an SM.
 constexpr int kTopkWarps = 4;
-constexpr int kPerLane = 64;  // candidates a lane can hold: 8192 blocks over 4 warps, 2048 over one
 
-template <int WPR>
+template <int WPR, int PL>
 __global__ void __launch_bounds__(kTopkWarps * 32) k_tree_topk(const __grid_constant__ TreeArgs a, const __nv_bfloat16* __restrict__ q_idx,
                                                                const __nv_bfloat16* __restrict__ k_idx) {
     constexpr int RPC = kTopkWarps / WPR;  // rows per CTA
-    constexpr int kCap = 17 * kPerLane + 4;  // survivors of a warp: at most topk + 1 lanes' candidates, and the last blocks
+    constexpr int kPerLane = PL;           // candidates a lane can hold
+    constexpr int kCap = 17 * PL + 4;      // survivors of a warp: at most topk + 1 lanes' candidates, and the last blocks
     __shared__ unsigned long long s_list[kTopkWarps * kCap];
     __shared__ int s_cnt[RPC], s_chosen[RPC][16];
     __shared__ uint32_t s_draft[RPC][4];
     __shared__ float s_kth[RPC][2];
-    pdl_wait();  // the maxima come from the scan
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slot = warp / WPR, sub = warp % WPR;
     const int R = a.T * a.H_kv, K1 = a.topk + 1;
@@ -343,6 +343,20 @@ __global__ void __launch_bounds__(kTopkWarps * 32) k_tree_topk(const __grid_cons
     if (live_row && row == 0 && sub == 0 && lane == 0 && (len != a.cache_len[b] || nodes != a.n_nodes[b]))
         raise_flag(a.status, MSA_DEV_BAD_BLOCK, 0xb31);
     const bool live = live_row && n < nodes;
+    pdl_wait();  // the maxima and the ancestor sets come from the scan
+    // candidates 4 (lane + 32 sub) + 128 WPR j + {0..3}; loaded before it is known which of them exist
+    const float* vals = a.bmax + ((int64_t)b * R + row) * a.bmax_ld;
+    float v[kPerLane];
+#pragma unroll
+    for (int j = 0; j < kPerLane / 4; ++j) {
+        const int c = 4 * (lane + 32 * sub) + 128 * WPR * j;
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live && c < a.bmax_ld) f = *reinterpret_cast<const float4*>(vals + c);
+        v[4 * j] = f.x;
+        v[4 * j + 1] = f.y;
+        v[4 * j + 2] = f.z;
+        v[4 * j + 3] = f.w;
+    }
     const unsigned long long anc = live ? a.anc[(int64_t)b * a.T + n] : 1ull;
     const int full = len / a.block_k;                                         // complete pages
     const int local = live ? (len + __popcll(anc) - 1) / a.block_k : 0;       // the node's own block
@@ -351,20 +365,7 @@ __global__ void __launch_bounds__(kTopkWarps * 32) k_tree_topk(const __grid_cons
     if (sub == 0 && lane == 0) s_cnt[slot] = 0;
     __syncthreads();
     unsigned long long* list = s_list + (size_t)slot * WPR * kCap;
-    const float* vals = a.bmax + ((int64_t)b * R + row) * a.bmax_ld;
     if (live) {
-        // candidates 4 (lane + 32 sub) + 128 WPR j + {0..3}
-        float v[kPerLane];
-#pragma unroll
-        for (int j = 0; j < kPerLane / 4; ++j) {
-            const int c = 4 * (lane + 32 * sub) + 128 * WPR * j;
-            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c < past) f = *reinterpret_cast<const float4*>(vals + c);
-            v[4 * j] = f.x;
-            v[4 * j + 1] = f.y;
-            v[4 * j + 2] = f.z;
-            v[4 * j + 3] = f.w;
-        }
         unsigned long long best = 0ull;
 #pragma unroll
         for (int j = 0; j < kPerLane / 4; ++j) {
@@ -500,10 +501,14 @@ cudaError_t run_tree_index(const TreeArgs& a, const void* q_idx, const void* k_i
     const int64_t rows = (int64_t)a.B * R;
     const auto* q = static_cast<const __nv_bfloat16*>(q_idx);
     const auto* k = static_cast<const __nv_bfloat16*>(k_idx);
-    // one warp per row up to 2048 blocks when the rows fill the device, else four
-    if (a.bmax_ld <= 32 * kPerLane && rows >= 16LL * num_sms)
-        return launch_pdl(k_tree_topk<1>, dim3((unsigned)((rows + 3) / 4)), dim3(kTopkWarps * 32), 0, st, a, q, k);
-    return launch_pdl(k_tree_topk<4>, dim3((unsigned)rows), dim3(kTopkWarps * 32), 0, st, a, q, k);
+    // one warp per row while 16 candidates a lane suffice (512 blocks), or 64 (2048) when the rows fill the device;
+    // else four warps
+    auto launch = [&](auto kern, int rpc) {
+        return launch_pdl(kern, dim3((unsigned)((rows + rpc - 1) / rpc)), dim3(kTopkWarps * 32), 0, st, a, q, k);
+    };
+    if (a.bmax_ld <= 512) return launch(k_tree_topk<1, 16>, 4);
+    if (a.bmax_ld <= 2048) return rows >= 16LL * num_sms ? launch(k_tree_topk<1, 64>, 4) : launch(k_tree_topk<4, 16>, 1);
+    return launch(k_tree_topk<4, 64>, 1);
 }
 
 }  // namespace msa

@@ -16,7 +16,7 @@
 // product, at most 2^-8 of each weight, and the products accumulate in fp32.
 //
 // NWG = 2 (more than 128 rows): two row tiles share K and V and alternate between the tensor cores and the
-// exponentials. Where the CTAs do not fill the device the union is split over `splits` CTAs and merged by
+// exponentials. NWG = 1: two S buffers, the next tile's S runs under this tile's exponentials. Where the CTAs do not fill the device the union is split over `splits` CTAs and merged by
 // k_tree_combine.
 #include <type_traits>
 
@@ -45,7 +45,10 @@ struct TreeAttnSmem {
     int before[kWords];
     float row_max[NWG][2][kRows];           // exchange between the two threads of a row
     float row_sum[NWG][2][kRows];
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], pv_done[2], drain;
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], drain;
+    // s_full, p_ready: one per S buffer (a row tile's, or with NWG = 1 alternate ones: a warp that runs a tile ahead of
+    // the others must not arrive twice on one barrier); pv_step: every PV (NWG = 1); pv_done: a row tile's last
+    uint64_t s_full[2], p_ready[2], pv_step, pv_done[2];
     int total;
     uint32_t tmem_base;
 };
@@ -72,7 +75,7 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
     constexpr int kTmaWarp = 8 * NWG, kMmaWarp = 8 * NWG + 1;
     constexpr uint32_t kHalf = kTile * 128;  // bytes of a 64-column half of a 128-row tile
     constexpr uint32_t kTileBytes = kTile * D * 2;
-    constexpr int kColO = 256;  // TMEM columns: S (then P) of row tile w at 128 w, O at 256 + 128 w
+    constexpr int kColO = 256;  // TMEM columns: S buffer i (then P) at 128 i, O of row tile w at 256 + 128 w
     constexpr int EPT = (kMaxEntries + NT - 1) / NT;  // list entries per thread
     extern __shared__ uint8_t tree_raw[];
     Sm& s = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(tree_raw) + 1023) & ~uintptr_t(1023));
@@ -126,6 +129,7 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
             mbar_init(&s.p_ready[x], 8);
             mbar_init(&s.pv_done[x], 1);
         }
+        mbar_init(&s.pv_step, 1);
         mbar_init(&s.drain, 1);
         fence_mbar_init();
     }
@@ -283,14 +287,15 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
         auto keys16 = [&](int j) { return (uint32_t)(tile_keys(t0 + j) + 15) / 16; };  // in the product's granularity
         auto issue_s = [&](int w, int j) {
             const uint32_t idesc = umma_idesc_bf16(kRows, 0, false, false) | (keys16(j) << 18);
+            const int buf = NWG == 1 ? (j & 1) : w;
             if (leader) {
                 const uint64_t qd = dq + w * (kTileBytes >> 4), kd = dk + (j & 1) * (kTileBytes >> 4);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint32_t off = ((ks / 4) * kHalf + (ks & 3) * 32) >> 4;
-                    umma_bf16(tmem + w * kTile, qd + off, kd + off, idesc, ks > 0);
+                    umma_bf16(tmem + buf * kTile, qd + off, kd + off, idesc, ks > 0);
                 }
-                umma_commit(&s.s_full[w]);
+                umma_commit(&s.s_full[buf]);
                 if (w == NWG - 1) umma_commit(&s.k_empty[j & 1]);
             }
             __syncwarp();
@@ -306,26 +311,32 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
         for (int j = 0; ok && j < n_tiles; ++j) {
             const bool more = j + 1 < n_tiles;
             const int steps = keys16(j);
-            ok = mbar_wait(&s.v_full[j & 1], (j >> 1) & 1, a.status, 0xc23);
-            if (ok && more) ok = mbar_wait(&s.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, a.status, 0xc22);
+            if (more) ok = mbar_wait(&s.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, a.status, 0xc22);
+            if (NWG == 1 && ok && more) {  // the next tile's S runs under this tile's exponentials
+                tc_fence_after();
+                issue_s(0, j + 1);
+            }
+            ok = ok && mbar_wait(&s.v_full[j & 1], (j >> 1) & 1, a.status, 0xc23);
 #pragma unroll
             for (int w = 0; w < NWG; ++w) {
-                ok = ok && mbar_wait(&s.p_ready[w], j & 1, a.status, 0xc24);
+                const int buf = NWG == 1 ? (j & 1) : w;
+                ok = ok && mbar_wait(&s.p_ready[buf], (NWG == 1 ? j >> 1 : j) & 1, a.status, 0xc24);
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
-                    const uint32_t tP = tmem + w * kTile, tO = tmem + kColO + w * kRows;
+                    const uint32_t tP = tmem + buf * kTile, tO = tmem + kColO + w * kRows;
                     const uint64_t vd = dv + (j & 1) * (kTileBytes >> 4);
 #pragma unroll
                     for (int ks = 0; ks < kTile / 16; ++ks)  // P of keys 64 .. 127 starts at column 64
                         if (ks < steps)
                             umma_bf16_tmem_a(tO, tP + (ks / 4) * 64 + (ks & 3) * 8, vd + ((ks * 16 * 128) >> 4), kIdescO,
                                              j > 0 || ks > 0);
+                    if (NWG == 1) umma_commit(&s.pv_step);
                     if (!more) umma_commit(&s.pv_done[w]);
                     if (w == NWG - 1) umma_commit(&s.v_empty[j & 1]);
                 }
                 __syncwarp();
-                if (more) issue_s(w, j + 1);
+                if (NWG == 2 && more) issue_s(w, j + 1);
             }
         }
         if (leader) umma_commit(&s.drain);
@@ -341,7 +352,7 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
         const int nl = (w * kRows + row) >> lg;
         const bool live = nl < mine;
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t tS = lane_addr + w * kTile + hf * 64, tO = lane_addr + kColO + w * kRows + hf * CW;
+        const uint32_t tO = lane_addr + kColO + w * kRows + hf * CW;
         const float sl2 = a.scale * 1.4426950408889634f;
         const uint64_t sl2x2 = f2_packf(sl2, sl2);
         const uint32_t* my_mask = reinterpret_cast<const uint32_t*>(s.mask) + ((nl >> 5) & 1);  // this row's word of an entry
@@ -350,7 +361,8 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
         uint64_t l2 = f2_packf(0.f, 0.f);  // the thread's part of the row's sum, two halves
         bool ok = true;
         for (int j = 0; ok && j < n_tiles; ++j) {
-            const int t = t0 + j, keys = tile_keys(t);
+            const int t = t0 + j, keys = tile_keys(t), buf = NWG == 1 ? (j & 1) : w;
+            const uint32_t tS = lane_addr + buf * kTile + hf * 64;
             const bool whole = t < page_tiles && keys == kTile;  // every column is a cached key
             // this thread's two chunks of 32 columns: all-ones or zero words; in a tile that is not whole the columns
             // one by one
@@ -381,8 +393,7 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
                 }
                 fence_proxy_async();
             }
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&s.s_full[w], j & 1, a.status, 0xc32));
-            // (S of this tile was issued after the PV of the one before: O is not being written)
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&s.s_full[buf], (NWG == 1 ? j >> 1 : j) & 1, a.status, 0xc32));
             tc_fence_after();
             const bool any = ok && __any_sync(0xffffffffu, (see[0] | see[1]) != 0u);
             // S is read twice, 32 columns at a time: all 64 in registers spilled, and the reloads took longer than this
@@ -419,6 +430,10 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
             // wait ran out: the two warps leave together)
             if (bar_red_or(pair_bar, 64, !ok || j == 0 || mx > mref + 8.f)) {
                 s.row_max[w][hf][row] = mx;
+                // O must not be written while it is rescaled. NWG = 2: this S was issued after the PV before it;
+                // NWG = 1: after the PV before that, so that the parity below is unambiguous
+                if (NWG == 1 && ok && j > 0)
+                    ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_step, (j - 1) & 1, a.status, 0xc33));
                 if (bar_red_or(pair_bar, 64, !ok)) {
                     ok = false;
                     break;
@@ -426,6 +441,7 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
                 const float m2 = fmaxf(mx, s.row_max[w][hf ^ 1][row]);
                 const bool up = j == 0 || m2 > mref + 8.f;
                 if (j > 0) {
+                    tc_fence_after();
                     const float f = up ? fast_exp2(mref - m2) : 1.f;
                     l2 = f2_mul(l2, f2_packf(f, f));
 #pragma unroll
@@ -484,14 +500,16 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.p_ready[w]);
+            if (lane == 0) mbar_arrive(&s.p_ready[buf]);
         }
         // -------------------------------------------------------------------- outputs
         // Through shared memory (Q and K are no longer read: the last S of both row tiles was issued before a last
         // PV), so that a warp writes whole rows: 32 rows of 16-byte pieces straight from the lanes took 4 us at the
         // end of every CTA.
         if (ok && n_tiles > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_done[w], 0, a.status, 0xc34));
+            bool done = false;
+            for (int i = 0; i < 32 && !done; ++i) done = mbar_try_wait(&s.pv_done[w], 0);  // before the timed wait's loads
+            ok = __all_sync(0xffffffffu, done || mbar_wait(&s.pv_done[w], 0, a.status, 0xc34));
             tc_fence_after();
         }
         float l0, l1;
