@@ -162,3 +162,43 @@ def test_streams_and_graphs():
     gr.replay()
     for a, b in zip(pools, want):
         assert torch.equal(a, b)
+
+
+def test_paged_cache_forks_and_compaction_on_the_device():
+    """PagedCache end to end: a prompt, two forks that diverge, one freed, the pool compacted; every sequence's
+    tokens stay what was appended."""
+    from block_sparse_attention_idx_b200.pages import PagedCache
+
+    g = torch.Generator(device=DEV).manual_seed(12)
+    dm = msa.MsaDims(1, 400, 8, 2, 64, 32, 32, 4)
+    c = PagedCache(dm, 40)
+    want = {}
+
+    def grow(seqs, T, rows=None):
+        x = [_bf(g, len(seqs), T, 2, 64), _bf(g, len(seqs), T, 2, 64), _bf(g, len(seqs), T, 32)]
+        c.append(seqs, *x, rows=rows)
+        for i, s in enumerate(seqs):
+            pick = list(range(T)) if rows is None else rows[i]
+            want[s] = [torch.cat([w, t[i, pick]]) for w, t in zip(want[s], x)]
+
+    def check():
+        for s, w in want.items():
+            pages = torch.tensor(c.page_list(s), device=DEV)
+            for pool, t in zip((c.k_pool, c.v_pool, c.k_idx_pool), w):
+                assert torch.equal(pool[pages].flatten(0, 1)[:c.length(s)], t)
+
+    a, z = c.new(), c.new()
+    for s in (a, z):
+        want[s] = [_bf(g, 0, 2, 64), _bf(g, 0, 2, 64), _bf(g, 0, 32)]
+    grow([z, a], 75)
+    b = c.fork(a)
+    want[b] = list(want[a])
+    grow([a, b], 7, rows=[[0, 2, 6], [1, 2, 3, 4]])
+    check()
+    c.free(z)
+    del want[z]
+    used = c.compact()
+    assert max(c.page_list(a) + c.page_list(b)) < used == 4
+    check()
+    grow([b, a], 33)
+    check()
