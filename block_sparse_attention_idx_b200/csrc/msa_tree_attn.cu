@@ -2,22 +2,23 @@
 // tokens of its virtual sequence (the cache, its ancestors, itself) that lie in the blocks of its list
 // blocks[b, node, r, :]: softmax(q . k * scale) v.
 //
-// Query-outer: one CTA holds 128 NWG rows (128 NWG / G nodes with the G heads of one group) and walks the
-// union of their selected pages, so that a page that several nodes chose, which is the rule (their queries
-// are near), is loaded once per CTA and no partial outputs are spilled; a node that did not choose a page is
-// masked there. The union is a bitmap over the sequence's blocks in shared memory, its order the block order,
-// each entry with the set of nodes that chose it. Keys go in tiles of 128 (128 / block_k pages); the last
-// tile is the drafted tokens, masked to each node's ancestors in its selected blocks.
+// Query-outer: one CTA holds 128 rows (128 / G nodes with the G heads of one group) and walks the union of their
+// selected pages, so that a page that several nodes chose, which is the rule (their queries are near), is loaded once
+// per CTA and no partial outputs are spilled; a node that did not choose a page is masked there. The union is a bitmap
+// over the sequence's blocks in shared memory, its order the block order, each entry with the set of nodes that chose
+// it. Keys go in tiles of 128 (128 / block_k pages); the last tile is the drafted tokens, masked to each node's
+// ancestors in its selected blocks.
 //
-// Per tile and 128 rows: S = Q K^T (tcgen05, M = N = 128) in TMEM; two threads share a row, 64 columns each: maximum,
-// exponentials (base 2) and sums in fp32, P as bf16 over S; O += P V accumulates in TMEM. The running maximum is
-// only raised, and O rescaled, when a row's maximum grows by more than 2^8: exponents stay far inside fp32 and bf16,
-// and most tiles rescale nothing. O and the LSE use the sum of the fp32 exponentials; P is rounded to bf16 for the
-// product, at most 2^-8 of each weight, and the products accumulate in fp32.
+// Per tile: S = Q K^T (tcgen05, M = N = 128) in TMEM; two threads share a row, 64 columns each: maximum, exponentials
+// (base 2) and sums in fp32, P as bf16 over S; O += P V accumulates in TMEM. The running maximum is only raised, and O
+// rescaled, when a row's maximum grows by more than 2^8: exponents stay far inside fp32 and bf16, and most tiles
+// rescale nothing. O and the LSE use the sum of the fp32 exponentials; P is rounded to bf16 for the product, at most
+// 2^-8 of each weight, and the products accumulate in fp32.
 //
-// NWG = 2 (more than 128 rows): two row tiles share K and V and alternate between the tensor cores and the
-// exponentials. NWG = 1: two S buffers, the next tile's S runs under this tile's exponentials. Where the CTAs do not fill the device the union is split over `splits` CTAs and merged by
-// k_tree_combine.
+// A CTA is a chain: S, exponentials, PV, next S. Two CTAs share an SM (256 TMEM columns, 113 KB and 96 registers a
+// thread each), so that one's products, loads, list building and output run under the other's exponentials. K and V
+// have one buffer each: K of the next tile arrives during this tile's exponentials, V during the next tile's. Where the
+// CTAs do not fill the device the union is split over `splits` CTAs and merged by k_tree_combine.
 #include <type_traits>
 
 #include "msa_tree.cuh"
@@ -30,32 +31,33 @@ constexpr int kRows = 128;
 constexpr int kMaxEntries = kTreeMaxT * 17;  // union of a CTA's lists
 constexpr int kWords = kTreeMaxBlocks / 32;
 
-template <int D, int NWG>
-struct TreeAttnSmem {
-    alignas(1024) uint8_t q[NWG][kRows * D * 2];  // with the start of k, at the end: outputs on their way out
-    alignas(1024) uint8_t k[2][kTile * D * 2];
-    alignas(1024) uint8_t v[2][kTile * D * 2];
-    unsigned long long mask[kMaxEntries];   // nodes of the CTA that chose the entry
-    unsigned long long anc[64], draft[64];  // ancestors of a node; drafted tokens that a node attends
-    unsigned long long in_block[4];         // nodes whose position lies in block len / block_k + i
-    int page[kMaxEntries];
-    int local[64];                          // local block of a node
-    uint32_t late[64];                      // blocks >= len / block_k in a node's list
-    uint32_t bits[kWords];
-    int before[kWords];
-    float row_max[NWG][2][kRows];           // exchange between the two threads of a row
-    float row_sum[NWG][2][kRows];
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], drain;
-    // s_full, p_ready: one per S buffer (a row tile's, or with NWG = 1 alternate ones: a warp that runs a tile ahead of
-    // the others must not arrive twice on one barrier); pv_step: every PV (NWG = 1); pv_done: a row tile's last
-    uint64_t s_full[2], p_ready[2], pv_step, pv_done[2];
-    int total;
-    uint32_t tmem_base;
+constexpr int kAttnThreads = 320;  // warps 0-7 softmax, 8 TMA, 9 MMA
+
+// What only the list building needs; it lies where V goes afterwards.
+struct TreeLists {
+    unsigned long long anc[64];       // ancestors of a node
+    unsigned long long in_block[4];   // nodes whose position lies in block len / block_k + i
+    int local[64];                    // local block of a node
+    uint32_t late[64];                // blocks >= len / block_k in a node's list
+    uint32_t bits[kWords];            // the union
+    int before[kWords];               // entries before a word's
 };
 
-// Threads: two softmax warpgroups per row tile, then a warpgroup with the TMA and the MMA warp (its other two warps
-// only help in the prologue): 640 threads of 96 registers with NWG = 2.
-constexpr int attn_threads(int nwg) { return (8 * nwg + 4) * 32; }
+template <int D>
+struct TreeAttnSmem {
+    alignas(1024) uint8_t q[kRows * D * 2];  // with k, at the end: outputs on their way out
+    alignas(1024) uint8_t k[kTile * D * 2];
+    alignas(1024) uint8_t v[kTile * D * 2];
+    unsigned long long mask[kMaxEntries];  // nodes of the CTA that chose the entry
+    unsigned long long draft[64];          // drafted tokens that a node attends
+    int page[kMaxEntries];
+    float row_max[2][kRows], row_sum[2][kRows];  // exchange between the two threads of a row
+    uint64_t k_full, k_empty, v_full, v_empty, s_full, p_ready, pv_done, drain;
+    int total, partial;
+    uint32_t tmem_base;
+};
+static_assert(sizeof(TreeAttnSmem<128>) + 1024 <= 113 * 1024, "two CTAs share an SM");
+static_assert(sizeof(TreeLists) <= kTile * 64 * 2, "the lists fit V's buffer");
 
 // Three-input maximum that keeps a NaN.
 __device__ __forceinline__ float max3n(float a, float b, float c) {
@@ -64,24 +66,24 @@ __device__ __forceinline__ float max3n(float a, float b, float c) {
     return m;
 }
 
-template <int D, int BK, int NWG>
-__global__ void __launch_bounds__(attn_threads(NWG), 1)
+template <int D, int BK>
+__global__ void __launch_bounds__(kAttnThreads, 2)
     k_tree_attn(const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
                 const __grid_constant__ CUtensorMap tm_kd, const __grid_constant__ CUtensorMap tm_vd,
                 const __grid_constant__ TreeArgs a, const __nv_bfloat16* __restrict__ q) {
-    using Sm = TreeAttnSmem<D, NWG>;
+    using Sm = TreeAttnSmem<D>;
     constexpr int TPT = kTile / BK;
-    constexpr int NT = attn_threads(NWG);
-    constexpr int kTmaWarp = 8 * NWG, kMmaWarp = 8 * NWG + 1;
+    constexpr int NT = kAttnThreads;
+    constexpr int kTmaWarp = 8, kMmaWarp = 9;
     constexpr uint32_t kHalf = kTile * 128;  // bytes of a 64-column half of a 128-row tile
-    constexpr uint32_t kTileBytes = kTile * D * 2;
-    constexpr int kColO = 256;  // TMEM columns: S buffer i (then P) at 128 i, O of row tile w at 256 + 128 w
+    constexpr int kColO = 128;  // TMEM columns: S (then P) at 0, O at 128
     constexpr int EPT = (kMaxEntries + NT - 1) / NT;  // list entries per thread
     extern __shared__ uint8_t tree_raw[];
     Sm& s = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(tree_raw) + 1023) & ~uintptr_t(1023));
+    TreeLists& ls = *reinterpret_cast<TreeLists*>(s.v);
     const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
     const int lg = a.lg_g, K1 = a.topk + 1;     // G = 2^lg heads per group
-    const int per_cta = (NWG * kRows) >> lg;  // nodes
+    const int per_cta = kRows >> lg;            // nodes
     auto list_of = [&](int e) { return (e * a.k1_inv) >> 16; };  // e / K1
     const int n_ct = (a.T + per_cta - 1) / per_cta;
     const int ct = blockIdx.x % n_ct, br = blockIdx.x / n_ct, r = br % a.H_kv, b = br / a.H_kv;
@@ -105,31 +107,48 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
         p1 = load_parent(a, b, lane + 32);
     }
     const int len = tree_len(a, b), nodes = tree_nodes(a, b);
-    for (int i = tid; i < NWG * kRows * (D / 8); i += NT) {
+    if (n0 >= nodes) {  // none of the CTA's nodes exists: zeros (its partial outputs are not read) and LSE -inf
+        if (tid == 0 && r == 0 && ct == 0 && split == 0 && (len != a.cache_len[b] || nodes != a.n_nodes[b]))
+            raise_flag(a.status, MSA_DEV_BAD_BLOCK, 0xc01);
+        const int rows = min(kRows, (a.T - n0) << lg);
+        auto out_row = [&](int i) { return ((int64_t)b * a.T + n0 + (i >> lg)) * a.H_q + (r << lg) + (i & ((1 << lg) - 1)); };
+        for (int i = tid; i < rows; i += NT) {
+            if (a.splits > 1) a.lse_part[split * n_rows + out_row(i)] = -INFINITY;
+            else if (a.lse) a.lse[out_row(i)] = -INFINITY;
+        }
+        for (int i = tid; a.splits == 1 && i < rows * (D / 8); i += NT) {
+            const int64_t o = out_row(i / (D / 8)) * D + (i % (D / 8)) * 8;
+            if (a.out_bf16) {
+                *reinterpret_cast<uint4*>(a.out_bf16 + o) = make_uint4(0, 0, 0, 0);
+            } else {
+                *reinterpret_cast<uint4*>(a.out + o) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(a.out + o + 4) = make_uint4(0, 0, 0, 0);
+            }
+        }
+        pdl_trigger();
+        return;
+    }
+    for (int i = tid; i < kRows * (D / 8); i += NT) {
         const int row = i / (D / 8), c = i % (D / 8), node = n0 + (row >> lg), h = row & ((1 << lg) - 1);
-        const uint32_t dst = smem_u32(s.q[0]) + (row / kRows) * (kRows * D * 2) + (c / 8) * kHalf +
-                             swz(row % kRows, (c % 8) * 16, 128);
+        const uint32_t dst = smem_u32(s.q) + (c / 8) * kHalf + swz(row, (c % 8) * 16, 128);
         const bool live = node < a.T;
         cp_async_16_zfill(dst, live ? q + (((int64_t)b * a.T + node) * a.H_q + (r << lg) + h) * D + c * 8 : q, live);
     }
     if (warp == kMmaWarp) {
-        tmem_alloc(&s.tmem_base, 512);
+        tmem_alloc(&s.tmem_base, 256);
         tmem_relinquish();
     }
-    for (int i = tid; i < kWords; i += NT) s.bits[i] = 0u;
+    for (int i = tid; i < kWords; i += NT) ls.bits[i] = 0u;
     for (int i = tid; i < kMaxEntries; i += NT) s.mask[i] = 0ull;
-    if (tid < 64) s.late[tid] = 0u;
+    if (tid < 64) ls.late[tid] = 0u;
     if (tid == 64) {
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(&s.k_full[x], 1);
-            mbar_init(&s.k_empty[x], 1);
-            mbar_init(&s.v_full[x], 1);
-            mbar_init(&s.v_empty[x], 1);
-            mbar_init(&s.s_full[x], 1);
-            mbar_init(&s.p_ready[x], 8);
-            mbar_init(&s.pv_done[x], 1);
-        }
-        mbar_init(&s.pv_step, 1);
+        mbar_init(&s.k_full, 1);
+        mbar_init(&s.k_empty, 1);
+        mbar_init(&s.v_full, 1);
+        mbar_init(&s.v_empty, 1);
+        mbar_init(&s.s_full, 1);
+        mbar_init(&s.p_ready, 8);
+        mbar_init(&s.pv_done, 1);
         mbar_init(&s.drain, 1);
         fence_mbar_init();
     }
@@ -147,14 +166,14 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int n = lane + 32 * x, loc = (len + __popcll(anc[x]) - 1) / BK;
-            s.anc[n] = anc[x];
-            s.local[n] = loc;
+            ls.anc[n] = anc[x];
+            ls.local[n] = loc;
             off[x] = n < nodes ? loc - full : -1;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t lo = __ballot_sync(0xffffffffu, off[0] == i), hi = __ballot_sync(0xffffffffu, off[1] == i);
-            if (lane == 0) s.in_block[i] = ((unsigned long long)hi << 32) | lo;
+            if (lane == 0) ls.in_block[i] = ((unsigned long long)hi << 32) | lo;
         }
     }
     __syncthreads();
@@ -165,13 +184,13 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
         pg[x] = 0;
         if (id[x] == -1 || nl >= mine) {
             id[x] = -1;
-        } else if (id[x] < -1 || id[x] > s.local[n0 + nl]) {
+        } else if (id[x] < -1 || id[x] > ls.local[n0 + nl]) {
             raise_flag(a.status, MSA_DEV_BAD_BLOCK, 0xc03);
             id[x] = -1;
         } else {
-            if (id[x] >= full) atomicOr(&s.late[nl], 1u << (id[x] - full));
+            if (id[x] >= full) atomicOr(&ls.late[nl], 1u << (id[x] - full));
             if (id[x] < npages) {
-                atomicOr(&s.bits[id[x] >> 5], 1u << (id[x] & 31));
+                atomicOr(&ls.bits[id[x] >> 5], 1u << (id[x] & 31));
                 pg[x] = tree_page(a, b, id[x], 0xc04);
             } else {
                 id[x] = -1;
@@ -182,7 +201,7 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
     if (warp == 0) {
         int sum = 0;
 #pragma unroll
-        for (int x = 0; x < kWords / 32; ++x) sum += __popc(s.bits[lane * (kWords / 32) + x]);
+        for (int x = 0; x < kWords / 32; ++x) sum += __popc(ls.bits[lane * (kWords / 32) + x]);
         int incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -192,10 +211,11 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
         int at = incl - sum;
 #pragma unroll
         for (int x = 0; x < kWords / 32; ++x) {
-            s.before[lane * (kWords / 32) + x] = at;
-            at += __popc(s.bits[lane * (kWords / 32) + x]);
+            ls.before[lane * (kWords / 32) + x] = at;
+            at += __popc(ls.bits[lane * (kWords / 32) + x]);
         }
         if (lane == 31) s.total = incl;
+        if (lane == 0) s.partial = npages > full && ((ls.bits[full >> 5] >> (full & 31)) & 1);
     } else if (tid >= 64 && tid < 128) {
         // drafted tokens that a node attends: its ancestors in its selected blocks
         const int nl = tid - 64;
@@ -203,8 +223,8 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
         if (nl < mine) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if ((s.late[nl] >> i) & 1) d |= s.in_block[i];
-            d &= s.anc[n0 + nl];
+                if ((ls.late[nl] >> i) & 1) d |= ls.in_block[i];
+            d &= ls.anc[n0 + nl];
         }
         s.draft[nl] = d;
     }
@@ -218,14 +238,13 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
 #pragma unroll
     for (int x = 0; x < EPT; ++x) {
         if (id[x] < 0) continue;
-        const int c = id[x], at = s.before[c >> 5] + __popc(s.bits[c >> 5] & ((1u << (c & 31)) - 1u));
+        const int c = id[x], at = ls.before[c >> 5] + __popc(ls.bits[c >> 5] & ((1u << (c & 31)) - 1u));
         if (at < e_lo || at >= e_hi) continue;
         atomicOr(&s.mask[at - e_lo], 1ull << list_of(tid + x * NT));
         s.page[at - e_lo] = pg[x];
     }
     // keys of the last page tile: the cache's last page, if chosen, holds len % block_k
-    const bool partial = npages > full && ((s.bits[full >> 5] >> (full & 31)) & 1);
-    const int last_keys = (U - (page_tiles - 1) * TPT) * BK - (partial ? BK - len % BK : 0);
+    const int last_keys = (U - (page_tiles - 1) * TPT) * BK - (s.partial ? BK - len % BK : 0);
     auto tile_keys = [&](int t) { return t < page_tiles - 1 ? kTile : t < page_tiles ? last_keys : nodes; };
     cp_async_wait_all();
     fence_proxy_async();
@@ -235,14 +254,13 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
     const uint32_t tmem = s.tmem_base;
     const int n_tiles = t1 - t0;
 
-    if (warp >= kTmaWarp) {
     if (warp == kTmaWarp) {
         // -------------------------------------------------------------------- TMA producer
         const bool leader = elect_one();
         int j = 0;
         bool ok = true;
         for (; j < n_tiles; ++j) {
-            const int st = j & 1, t = t0 + j;
+            const int t = t0 + j;
             const bool drafted = t == page_tiles;
             const int cnt = drafted ? 1 : min(TPT, U - t * TPT);
             const uint32_t bytes = drafted ? 64u * D * 2 : (uint32_t)cnt * BK * D * 2;
@@ -251,11 +269,11 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
             for (int x = 0; x < TPT; ++x) rows[x] = x < cnt && !drafted ? s.page[t * TPT + x - e_lo] * BK : 0;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
-                uint64_t* fullb = kv ? &s.v_full[st] : &s.k_full[st];
-                if (ok && j >= 2) ok = mbar_wait(kv ? &s.v_empty[st] : &s.k_empty[st], ((j >> 1) - 1) & 1, a.status, 0xc11);
+                uint64_t* fullb = kv ? &s.v_full : &s.k_full;
+                if (ok && j > 0) ok = mbar_wait(kv ? &s.v_empty : &s.k_empty, (j - 1) & 1, a.status, 0xc11);
                 if (!ok) break;
                 if (leader) {
-                    uint8_t* dst = kv ? s.v[st] : s.k[st];
+                    uint8_t* dst = kv ? s.v : s.k;
                     mbar_arrive_expect_tx(fullb, bytes);
 #pragma unroll
                     for (int h = 0; h < D / 64; ++h) {
@@ -274,85 +292,63 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
             if (!ok) break;
         }
         // no copy of ours may still be landing when the CTA leaves
-        for (int m = max(0, j - 2); m < j; ++m) {
-            mbar_wait(&s.k_full[m & 1], (m >> 1) & 1, a.status, 0xc12);
-            mbar_wait(&s.v_full[m & 1], (m >> 1) & 1, a.status, 0xc13);
+        if (j > 0) {
+            mbar_wait(&s.k_full, (j - 1) & 1, a.status, 0xc12);
+            mbar_wait(&s.v_full, (j - 1) & 1, a.status, 0xc13);
         }
     } else if (warp == kMmaWarp) {
         // -------------------------------------------------------------------- MMA issuer
         const bool leader = elect_one();
-        const uint64_t dq = umma_sdesc(smem_u32(s.q[0]), 16, 1024, 2), dk = umma_sdesc(smem_u32(s.k[0]), 16, 1024, 2);
-        const uint64_t dv = umma_sdesc(smem_u32(s.v[0]), kHalf, 1024, 2);
+        const uint64_t dq = umma_sdesc(smem_u32(s.q), 16, 1024, 2), dk = umma_sdesc(smem_u32(s.k), 16, 1024, 2);
+        const uint64_t dv = umma_sdesc(smem_u32(s.v), kHalf, 1024, 2);
         constexpr uint32_t kIdescO = umma_idesc_bf16(kRows, D, false, true);
-        auto keys16 = [&](int j) { return (uint32_t)(tile_keys(t0 + j) + 15) / 16; };  // in the product's granularity
-        auto issue_s = [&](int w, int j) {
-            const uint32_t idesc = umma_idesc_bf16(kRows, 0, false, false) | (keys16(j) << 18);
-            const int buf = NWG == 1 ? (j & 1) : w;
-            if (leader) {
-                const uint64_t qd = dq + w * (kTileBytes >> 4), kd = dk + (j & 1) * (kTileBytes >> 4);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = ((ks / 4) * kHalf + (ks & 3) * 32) >> 4;
-                    umma_bf16(tmem + buf * kTile, qd + off, kd + off, idesc, ks > 0);
-                }
-                umma_commit(&s.s_full[buf]);
-                if (w == NWG - 1) umma_commit(&s.k_empty[j & 1]);
-            }
-            __syncwarp();
-        };
         bool ok = true;
-        if (n_tiles > 0) {
-            ok = mbar_wait(&s.k_full[0], 0, a.status, 0xc21);
-            tc_fence_after();
-#pragma unroll
-            for (int w = 0; w < NWG; ++w)
-                if (ok) issue_s(w, 0);
-        }
-        for (int j = 0; ok && j < n_tiles; ++j) {
-            const bool more = j + 1 < n_tiles;
-            const int steps = keys16(j);
-            if (more) ok = mbar_wait(&s.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, a.status, 0xc22);
-            if (NWG == 1 && ok && more) {  // the next tile's S runs under this tile's exponentials
-                tc_fence_after();
-                issue_s(0, j + 1);
-            }
-            ok = ok && mbar_wait(&s.v_full[j & 1], (j >> 1) & 1, a.status, 0xc23);
-#pragma unroll
-            for (int w = 0; w < NWG; ++w) {
-                const int buf = NWG == 1 ? (j & 1) : w;
-                ok = ok && mbar_wait(&s.p_ready[buf], (NWG == 1 ? j >> 1 : j) & 1, a.status, 0xc24);
+        for (int j = 0; ok && j <= n_tiles; ++j) {  // PV of tile j - 1, S of tile j
+            if (j > 0) {
+                const int steps = (tile_keys(t0 + j - 1) + 15) / 16;
+                ok = mbar_wait(&s.v_full, (j - 1) & 1, a.status, 0xc23) && mbar_wait(&s.p_ready, (j - 1) & 1, a.status, 0xc24);
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
-                    const uint32_t tP = tmem + buf * kTile, tO = tmem + kColO + w * kRows;
-                    const uint64_t vd = dv + (j & 1) * (kTileBytes >> 4);
 #pragma unroll
                     for (int ks = 0; ks < kTile / 16; ++ks)  // P of keys 64 .. 127 starts at column 64
                         if (ks < steps)
-                            umma_bf16_tmem_a(tO, tP + (ks / 4) * 64 + (ks & 3) * 8, vd + ((ks * 16 * 128) >> 4), kIdescO,
-                                             j > 0 || ks > 0);
-                    if (NWG == 1) umma_commit(&s.pv_step);
-                    if (!more) umma_commit(&s.pv_done[w]);
-                    if (w == NWG - 1) umma_commit(&s.v_empty[j & 1]);
+                            umma_bf16_tmem_a(tmem + kColO, tmem + (ks / 4) * 64 + (ks & 3) * 8, dv + ((ks * 16 * 128) >> 4), kIdescO,
+                                             j > 1 || ks > 0);
+                    umma_commit(&s.v_empty);
+                    if (j == n_tiles) umma_commit(&s.pv_done);
                 }
                 __syncwarp();
-                if (NWG == 2 && more) issue_s(w, j + 1);
+            }
+            if (j < n_tiles) {
+                ok = mbar_wait(&s.k_full, j & 1, a.status, 0xc22);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t idesc = umma_idesc_bf16(kRows, 0, false, false) | ((uint32_t)(tile_keys(t0 + j) + 15) / 16 << 18);
+                if (leader) {
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = ((ks / 4) * kHalf + (ks & 3) * 32) >> 4;
+                        umma_bf16(tmem, dq + off, dk + off, idesc, ks > 0);
+                    }
+                    umma_commit(&s.s_full);
+                    umma_commit(&s.k_empty);
+                }
+                __syncwarp();
             }
         }
         if (leader) umma_commit(&s.drain);
         mbar_wait(&s.drain, 0, a.status, 0xc25);
-    }
     } else {
         // -------------------------------------------------------------------- softmax: two threads per row
-        // Thread (w, hf, row): columns 64 hf .. 64 hf + 63 of row tile w's S. Four warps per scheduler hide each
-        // other's latencies (one thread per row, 128 columns each, issued 0.34 instructions a cycle).
+        // Thread (hf, row): columns 64 hf .. 64 hf + 63 of S.
         constexpr int CW = D / 2;  // output columns of a thread
-        const int w = warp >> 3, hf = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
-        const uint32_t pair_bar = 1 + w * 4 + (warp & 3);  // the two warps of these 32 rows
-        const int nl = (w * kRows + row) >> lg;
+        const int hf = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t pair_bar = 1 + (warp & 3);  // the two warps of these 32 rows
+        const int nl = row >> lg;
         const bool live = nl < mine;
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t tO = lane_addr + kColO + w * kRows + hf * CW;
+        const uint32_t tS = lane_addr + hf * 64, tO = lane_addr + kColO + hf * CW;
         const float sl2 = a.scale * 1.4426950408889634f;
         const uint64_t sl2x2 = f2_packf(sl2, sl2);
         const uint32_t* my_mask = reinterpret_cast<const uint32_t*>(s.mask) + ((nl >> 5) & 1);  // this row's word of an entry
@@ -361,8 +357,7 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
         uint64_t l2 = f2_packf(0.f, 0.f);  // the thread's part of the row's sum, two halves
         bool ok = true;
         for (int j = 0; ok && j < n_tiles; ++j) {
-            const int t = t0 + j, keys = tile_keys(t), buf = NWG == 1 ? (j & 1) : w;
-            const uint32_t tS = lane_addr + buf * kTile + hf * 64;
+            const int t = t0 + j, keys = tile_keys(t);
             const bool whole = t < page_tiles && keys == kTile;  // every column is a cached key
             // this thread's two chunks of 32 columns: all-ones or zero words; in a tile that is not whole the columns
             // one by one
@@ -382,18 +377,20 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
                 see[0] = (uint32_t)d;
                 see[1] = (uint32_t)(d >> 32);
             }
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&s.s_full, j & 1, a.status, 0xc32));
+            // (this S was issued after the PV of the tile before: O is not being written)
             // rows of V behind the tile's last key, up to the product's depth, hold whatever the page or the
-            // stage held before: zeros, so that P = 0 there gives 0 even against NaN
+            // buffer held before: zeros, so that P = 0 there gives 0 even against NaN. (After the wait for S: before it, a warp
+            // whose rows are masked could be a tile ahead, where V's barrier does not tell this tile from the one before.)
             const int pad = ((keys + 15) & ~15) - keys;
-            if (w == 0 && pad) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&s.v_full[j & 1], (j >> 1) & 1, a.status, 0xc31));
+            if (ok && pad) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&s.v_full, j & 1, a.status, 0xc31));
                 for (int i = hf * kRows + row; ok && i < pad * (D / 8); i += 2 * kRows) {
                     const int vr = keys + i / (D / 8), c = i % (D / 8);
-                    *reinterpret_cast<uint4*>(s.v[j & 1] + (c / 8) * kHalf + swz(vr, (c % 8) * 16, 128)) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(s.v + (c / 8) * kHalf + swz(vr, (c % 8) * 16, 128)) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async();
             }
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&s.s_full[buf], (NWG == 1 ? j >> 1 : j) & 1, a.status, 0xc32));
             tc_fence_after();
             const bool any = ok && __any_sync(0xffffffffu, (see[0] | see[1]) != 0u);
             // S is read twice, 32 columns at a time: all 64 in registers spilled, and the reloads took longer than this
@@ -429,16 +426,12 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
             // the running maximum, common to the row's two threads, is only touched when one of the 64 has to (or a
             // wait ran out: the two warps leave together)
             if (bar_red_or(pair_bar, 64, !ok || j == 0 || mx > mref + 8.f)) {
-                s.row_max[w][hf][row] = mx;
-                // O must not be written while it is rescaled. NWG = 2: this S was issued after the PV before it;
-                // NWG = 1: after the PV before that, so that the parity below is unambiguous
-                if (NWG == 1 && ok && j > 0)
-                    ok = __all_sync(0xffffffffu, mbar_wait(&s.pv_step, (j - 1) & 1, a.status, 0xc33));
+                s.row_max[hf][row] = mx;
                 if (bar_red_or(pair_bar, 64, !ok)) {
                     ok = false;
                     break;
                 }
-                const float m2 = fmaxf(mx, s.row_max[w][hf ^ 1][row]);
+                const float m2 = fmaxf(mx, s.row_max[hf ^ 1][row]);
                 const bool up = j == 0 || m2 > mref + 8.f;
                 if (j > 0) {
                     tc_fence_after();
@@ -500,24 +493,23 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.p_ready[buf]);
+            if (lane == 0) mbar_arrive(&s.p_ready);
         }
         // -------------------------------------------------------------------- outputs
-        // Through shared memory (Q and K are no longer read: the last S of both row tiles was issued before a last
-        // PV), so that a warp writes whole rows: 32 rows of 16-byte pieces straight from the lanes took 4 us at the
+        // Through shared memory (Q and K are no longer read: the last S was issued before the last PV), so that a warp writes whole rows: 32 rows of 16-byte pieces straight from the lanes took 4 us at the
         // end of every CTA.
         if (ok && n_tiles > 0) {
             bool done = false;
-            for (int i = 0; i < 32 && !done; ++i) done = mbar_try_wait(&s.pv_done[w], 0);  // before the timed wait's loads
-            ok = __all_sync(0xffffffffu, done || mbar_wait(&s.pv_done[w], 0, a.status, 0xc34));
+            for (int i = 0; i < 32 && !done; ++i) done = mbar_try_wait(&s.pv_done, 0);  // before the timed wait's loads
+            ok = __all_sync(0xffffffffu, done || mbar_wait(&s.pv_done, 0, a.status, 0xc34));
             tc_fence_after();
         }
         float l0, l1;
         f2_unpack(l2, l0, l1);
-        s.row_sum[w][hf][row] = l0 + l1;
+        s.row_sum[hf][row] = l0 + l1;
         bar_sync_named(pair_bar, 64);
         if (ok) {
-            const float l = s.row_sum[w][0][row] + s.row_sum[w][1][row];
+            const float l = s.row_sum[0][row] + s.row_sum[1][row];
             const bool part = a.splits > 1;
             const bool has = l > 0.f || l != l;  // a NaN sum stays NaN
             const float inv = has ? 1.f / l : 0.f;
@@ -527,11 +519,11 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
                 return ((int64_t)b * a.T + n0 + (i >> lg)) * a.H_q + (r << lg) + (i & ((1 << lg) - 1));
             };
             const bool write = hf == 0 && n0 + nl < a.T;
-            if (write && part) a.lse_part[split * n_rows + out_row(w * kRows + row)] = lse;
-            if (write && !part && a.lse) a.lse[out_row(w * kRows + row)] = lse;
+            if (write && part) a.lse_part[split * n_rows + out_row(row)] = lse;
+            if (write && !part && a.lse) a.lse[out_row(row)] = lse;
             if (!part || n_tiles > 0) {
                 const bool half = !part && a.out_bf16;
-                uint8_t* stage = s.q[0] + warp * (32 * CW * 4);
+                uint8_t* stage = s.q + warp * (32 * CW * 4);
                 const int lp = (half ? 1 : 2) + (CW == 64 ? 2 : 1), pieces = 1 << lp;  // 16-byte pieces of a row
                 const int sw = pieces - 1 < 7 ? pieces - 1 : 7;
 #pragma unroll
@@ -560,7 +552,7 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
                 }
                 __syncwarp();
                 for (int i = lane; i < 32 << lp; i += 32) {
-                    const int rr = i >> lp, pc = i & (pieces - 1), ri = w * kRows + (warp & 3) * 32 + rr;
+                    const int rr = i >> lp, pc = i & (pieces - 1), ri = (warp & 3) * 32 + rr;
                     if (n0 + (ri >> lg) >= a.T) break;
                     const uint4 val = *reinterpret_cast<const uint4*>(stage + (rr << (lp + 4)) + ((pc ^ (rr & sw)) << 4));
                     uint8_t* dst = half ? reinterpret_cast<uint8_t*>(a.out_bf16 + out_row(ri) * D + hf * CW)
@@ -574,7 +566,7 @@ __global__ void __launch_bounds__(attn_threads(NWG), 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 256);
     pdl_trigger();
 }
 
@@ -620,10 +612,8 @@ __global__ void __launch_bounds__(256) k_tree_combine(const __grid_constant__ Tr
     if (lane == 0 && a.lse) a.lse[w] = z == 0.f ? -INFINITY : mx + logf(z);
 }
 
-// row tiles of 128 (node, head) rows that one CTA holds
-int tree_wg(int T, int G) { return T * G > kRows ? 2 : 1; }
 int tree_ctas(int B, int T, int H_q, int H_kv) {
-    const int G = H_q / H_kv, per = tree_wg(T, G) * kRows / G;
+    const int per = kRows / (H_q / H_kv);  // nodes per CTA
     return B * H_kv * ((T + per - 1) / per);
 }
 
@@ -633,7 +623,7 @@ int tree_ctas(int B, int T, int H_q, int H_kv) {
 // of a single node's list.
 int tree_attn_splits(int B, int T, int H_q, int H_kv, int block_k, int topk, int num_sms) {
     const int tpt = kTile / block_k, tiles = (topk + 1 + tpt - 1) / tpt + 1;
-    return std::max(1, std::min({tiles, num_sms / tree_ctas(B, T, H_q, H_kv), 32}));
+    return std::max(1, std::min({tiles, 2 * num_sms / tree_ctas(B, T, H_q, H_kv), 32}));
 }
 size_t tree_attn_ws_bytes(int B, int T, int H_q, int d, int splits) {
     if (splits <= 1) return 0;
@@ -643,7 +633,6 @@ size_t tree_attn_ws_bytes(int B, int T, int H_q, int d, int splits) {
 
 cudaError_t run_tree_attn(const TreeArgs& a, const void* q, const void* k, const void* v, const void* k_pool,
                           const void* v_pool, cudaStream_t st) {
-    const int G = a.H_q / a.H_kv;
     CUtensorMap kp, vp, kd, vd;
     const uint64_t es = 2, row = (uint64_t)a.H_kv * a.d * es;
     const uint64_t dims[4] = {(uint64_t)a.d, (uint64_t)a.H_kv, (uint64_t)a.T, (uint64_t)a.B};
@@ -654,20 +643,16 @@ cudaError_t run_tree_attn(const TreeArgs& a, const void* q, const void* k, const
         !make_tmap_3d(&vp, v_pool, a.d, a.H_kv, slots, a.d * es, row, 64, 1, a.block_k, 128) ||
         !make_tmap_4d(&kd, k, dims, strides, box, 128) || !make_tmap_4d(&vd, v, dims, strides, box, 128))
         return cudaErrorInvalidValue;
-    const int wg = tree_wg(a.T, G);
     const dim3 grid(tree_ctas(a.B, a.T, a.H_q, a.H_kv), a.splits);
     const auto* qb = static_cast<const __nv_bfloat16*>(q);
-    auto launch = [&](auto kern, size_t bytes) -> cudaError_t {
-        const size_t smem = std::max<size_t>(bytes + 1024, 120 * 1024);  // one CTA (512 TMEM columns) per SM
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        kern<<<grid, attn_threads(wg), smem, st>>>(kp, vp, kd, vd, a, qb);
-        return cudaGetLastError();
-    };
     auto pick = [&](auto d_c, auto bk_c) -> cudaError_t {
         constexpr int D = decltype(d_c)::value, BK = decltype(bk_c)::value;
-        return wg == 2 ? launch(k_tree_attn<D, BK, 2>, sizeof(TreeAttnSmem<D, 2>))
-                       : launch(k_tree_attn<D, BK, 1>, sizeof(TreeAttnSmem<D, 1>));
+        const size_t smem = std::max<size_t>(sizeof(TreeAttnSmem<D>) + 1024, 100 * 1024);  // at most two CTAs an SM
+        auto kern = k_tree_attn<D, BK>;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        kern<<<grid, kAttnThreads, smem, st>>>(kp, vp, kd, vd, a, qb);
+        return cudaGetLastError();
     };
     using I32 = std::integral_constant<int, 32>;
     using I64 = std::integral_constant<int, 64>;
