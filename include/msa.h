@@ -331,7 +331,7 @@ MSA_API msa_status msa_kl_dense_fwd_grad(const msa_dims *dims, const void *q, co
  *                y may be x itself (same stride and type: in place); any other overlap of an output with an
  *                input or another output gives MSA_ERR_INVALID_ARG (strided tensors of different strides
  *                count as overlapping where their address ranges do)
- *     inv_freq   fp64 [rot / 2] device, |inv_freq| below 2^31
+ *     inv_freq   fp64 [rot / 2] device, finite
  *     heads      1 .. 4096;  dim in {32, 64, 128};  rot even, 2 .. dim;  amp finite
  *   tokens     0 .. 2^31 - 1 (0 enqueues nothing)
  *   positions  int32 [tokens] device, any sign; NULL: token t has position t
@@ -434,7 +434,8 @@ MSA_API msa_status msa_tree_index_topk(const msa_dims *dims, const msa_pages *pa
  *   lse    fp32 [B, T, H_q] or NULL: natural-log sum-exp of the scaled logits                     (output)
  * A row that sees no token has output 0 and LSE -inf. Entries of V (of the drafted tokens of existing nodes and
  * of the cached tokens below cache_len) must be finite: nodes share a block's product, so an infinity or NaN
- * there may reach nodes that did not select it. What lies behind the last token, in pages or in
+ * there may reach nodes that did not select it. A NaN or infinite logit makes the rows that see it NaN, and
+ * only those. What lies behind the last token, in pages or in
  * the drafted arrays, may be anything.
  */
 MSA_API msa_status msa_tree_sparse_attn(const msa_dims *dims, const msa_pages *pages, const msa_tree *tree,

@@ -33,9 +33,9 @@ def rope(x: torch.Tensor, inv_freq: torch.Tensor, amp: float, positions, interle
 
 def gather_pages(pool: torch.Tensor, table_row, n: int) -> torch.Tensor:
     """The first n tokens of a sequence from its pages, in order."""
-    bk = pool.shape[1]
-    rows = [pool[int(table_row[p // bk]), p % bk] for p in range(n)]
-    return torch.stack(rows) if rows else pool[0, :0]
+    bk, p = pool.shape[1], torch.arange(n, device=pool.device)
+    table = torch.as_tensor(table_row, device=pool.device).long()
+    return pool[table[p // bk], p % bk] if n else pool[0, :0]
 
 
 def path(parents_row, n: int) -> list[int]:

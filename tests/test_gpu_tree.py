@@ -328,3 +328,81 @@ def test_speculative_step_end_to_end():
     c.q, c.k, c.v = _bf(g, *c.q.shape), _bf(g, *c.k.shape), _bf(g, *c.v.shape)
     c.q_idx, c.k_idx = _grid(g, *c.q_idx.shape), _grid(g, *c.k_idx.shape)
     _run(c)
+
+
+def test_many_sequences_some_without_a_cache_or_nodes():
+    """More sequences than SMs: the ragged work list, ancestor sets by several sequences per CTA."""
+    g = torch.Generator().manual_seed(3)
+    B = 317
+    lens = torch.randint(0, 90, (B,), generator=g).tolist()
+    nn = torch.randint(0, 4, (B,), generator=g).tolist()
+    c = Case(lens, 3, H_q=4, H_kv=2, d=64, di=32, bk=32, topk=2, n_nodes=nn, seed=21)
+    _run(c)
+
+
+@pytest.mark.parametrize("bk,L", [(32, 262144), (128, 262143), (64, 140001)])
+def test_largest_block_counts(bk, L):
+    """Up to the 8192 blocks of a sequence: every Top-k variant, lists spread over the whole page table."""
+    c = Case([L - 5, L // 2], 2, H_q=16, H_kv=2, d=64, di=32, bk=bk, topk=16, seed=bk, N=L)
+    _run(c)
+
+
+def test_nan_and_infinite_values_stay_with_the_rows_that_see_them():
+    """A NaN query, a NaN and an infinite key in a page that one node selects, a NaN key of a drafted token: only the
+    rows that see them are NaN, the others as without."""
+    c = Case([9 * 32 + 4], 4, H_q=8, H_kv=2, d=64, di=32, bk=32, topk=4, kind="roots", seed=31)
+    lists = torch.full((1, 4, 2, 5), -1, dtype=I32, device=DEV)
+    for n in range(4):
+        lists[0, n, :, :4] = torch.tensor([0, 1, 2 + n, 9], device=DEV)  # block 2 + n is node n's alone
+    good, glse = c.attend(lists, want_lse=True)
+    c.check_attention(lists, good, glse)
+    c.q[0, 0, 3] = NAN
+    c.kp[int(c.table[0, 3]), 5, 1] = NAN           # block 3, group 1: node 1
+    c.kp[int(c.table[0, 4]), 31, 0, 7] = float("inf")  # block 4, group 0: node 2
+    c.k[0, 3, 0] = NAN                             # node 3's own key, group 0
+    out, lse = c.attend(lists, want_lse=True)
+    bad = torch.zeros(4, 8, dtype=torch.bool, device=DEV)
+    bad[0, 3] = True
+    bad[1, 4:], bad[2, :4], bad[3, :4] = True, True, True
+    # (q . k with one infinite element is +-inf by the sign of q's: -inf is a weight of zero, not a NaN)
+    minus = c.q[0, 2, :4, 7] < 0
+    nan = torch.isnan(out[0]).all(-1) & torch.isnan(lse[0])
+    assert torch.equal(nan[:2], bad[:2]) and torch.equal(nan[3], bad[3])
+    assert torch.equal(nan[2, 4:], bad[2, 4:]) and torch.equal(nan[2, :4], ~minus)
+    assert torch.equal(out[0][~bad], good[0][~bad]) and torch.equal(lse[0][~bad], glse[0][~bad])
+    assert torch.isfinite(out[0, 2, :4][minus]).all()
+
+
+def test_two_calls_at_once_on_two_streams():
+    a = Case([700, 300], 8, H_q=64, H_kv=4, d=128, di=64, bk=128, topk=4, seed=41)
+    b = Case([90, 1000, 5], 5, H_q=8, H_kv=2, d=64, di=32, bk=32, topk=3, seed=42)
+    want = []
+    for c in (a, b):
+        blocks = c.select()
+        want.append((blocks, c.attend(blocks)[0]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        got = []
+        for c, s in zip((a, b), streams):
+            blocks = c.select(stream=s)
+            got.append((blocks, c.attend(blocks, stream=s)[0]))
+        torch.cuda.synchronize()
+        for (x, y), (u, v) in zip(got, want):
+            assert torch.equal(x, u) and torch.equal(y, v)
+
+
+def test_callers_workspace_and_output():
+    c = Case([300, 40], 3, seed=51)
+    ws = msa.tree_workspace(msa.MSA_OP_TREE_ATTN, c.dm, 3, DEV)
+    blocks = c.select()
+    out = torch.full((2, 3, 8, 64), 7.0, device=DEV)
+    o, lse = c.attend(blocks, out=out, ws=ws)
+    assert o is out and lse is None and torch.equal(out, c.attend(blocks)[0])
+    with pytest.raises(msa.MsaError) as e:
+        c.attend(blocks, ws=torch.empty(128, dtype=torch.uint8, device=DEV))
+    assert e.value.code == msa.MSA_ERR_WORKSPACE
+    with pytest.raises(ValueError, match="out: expected"):
+        c.attend(blocks, out=out, out_dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="parents"):
+        msa.msa_tree_index_topk(c.dm, c.pages, msa.MsaTree(c.parents[:1], c.n_nodes), c.q_idx, c.k_idx, c.kip)
