@@ -6,8 +6,8 @@
 // selected pages, so that a page that several nodes chose, which is the rule (their queries are near), is loaded once
 // per CTA and no partial outputs are spilled; a node that did not choose a page is masked there. The union is a bitmap
 // over the sequence's blocks in shared memory, its order the block order, each entry with the set of nodes that chose
-// it. Keys go in tiles of 128 (128 / block_k pages); the last tile is the drafted tokens, masked to each node's
-// ancestors in its selected blocks.
+// it. Keys go in tiles of 128: first the drafted tokens, masked to each node's ancestors in its selected blocks, whose
+// loads run while the union is built, then the pages, 128 / block_k a tile.
 //
 // Per tile: S = Q K^T (tcgen05, M = N = 128) in TMEM; two threads share a row, 64 columns each: maximum, exponentials
 // (base 2) and sums in fp32, P as bf16 over S; O += P V accumulates in TMEM. The running maximum is only raised, and O
@@ -33,7 +33,8 @@ constexpr int kWords = kTreeMaxBlocks / 32;
 
 constexpr int kAttnThreads = 320;  // warps 0-7 softmax, 8 TMA, 9 MMA
 
-// What only the list building needs; it lies where V goes afterwards.
+// What only the list building needs; it lies in V's buffer, behind the 64 rows that the drafted tokens' load fills
+// meanwhile (in the first 64-column half).
 struct TreeLists {
     unsigned long long anc[64];       // ancestors of a node
     unsigned long long in_block[4];   // nodes whose position lies in block len / block_k + i
@@ -57,7 +58,7 @@ struct TreeAttnSmem {
     uint32_t tmem_base;
 };
 static_assert(sizeof(TreeAttnSmem<128>) + 1024 <= 113 * 1024, "two CTAs share an SM");
-static_assert(sizeof(TreeLists) <= kTile * 64 * 2, "the lists fit V's buffer");
+static_assert(sizeof(TreeLists) <= 64 * 128, "the lists fit V's rows 64 .. 127");
 
 // Three-input maximum that keeps a NaN.
 __device__ __forceinline__ float max3n(float a, float b, float c) {
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     constexpr int EPT = (kMaxEntries + NT - 1) / NT;  // list entries per thread
     extern __shared__ uint8_t tree_raw[];
     Sm& s = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(tree_raw) + 1023) & ~uintptr_t(1023));
-    TreeLists& ls = *reinterpret_cast<TreeLists*>(s.v);
+    TreeLists& ls = *reinterpret_cast<TreeLists*>(s.v + 64 * 128);
     const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
     const int lg = a.lg_g, K1 = a.topk + 1;     // G = 2^lg heads per group
     const int per_cta = kRows >> lg;            // nodes
@@ -101,6 +102,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         const int nl = list_of(e);
         id[x] = e < n_ent ? a.blocks[(((int64_t)b * a.T + n0 + nl) * a.H_kv + r) * K1 + e - nl * K1] : -1;
     }
+    // the pages of the listed blocks, before it is known which of them count
+#pragma unroll
+    for (int x = 0; x < EPT; ++x)
+        pg[x] = (unsigned)id[x] < (unsigned)a.cols ? a.page_table[(int64_t)b * a.cols + id[x]] : -1;
     int p0 = -1, p1 = -1;
     if (warp == kTmaWarp) {
         p0 = load_parent(a, b, lane);
@@ -128,6 +133,29 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         pdl_trigger();
         return;
     }
+    if (warp == kTmaWarp && elect_one()) {
+        mbar_init(&s.k_full, 1);
+        mbar_init(&s.k_empty, 1);
+        mbar_init(&s.v_full, 1);
+        mbar_init(&s.v_empty, 1);
+        mbar_init(&s.s_full, 1);
+        mbar_init(&s.p_ready, 8);
+        mbar_init(&s.pv_done, 1);
+        mbar_init(&s.drain, 1);
+        fence_mbar_init();
+        if (split == 0) {  // the drafted tokens' tile
+            mbar_arrive_expect_tx(&s.k_full, 64u * D * 2);
+            mbar_arrive_expect_tx(&s.v_full, 64u * D * 2);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+                tma_load_4d(s.k + h * kHalf, &tm_kd, &s.k_full, 64 * h, r, 0, b);
+                tma_load_4d(s.v + h * kHalf, &tm_vd, &s.v_full, 64 * h, r, 0, b);
+            }
+        }
+        prefetch_tmap(&tm_kp);
+        prefetch_tmap(&tm_vp);
+    }
+    __syncwarp();
     for (int i = tid; i < kRows * (D / 8); i += NT) {
         const int row = i / (D / 8), c = i % (D / 8), node = n0 + (row >> lg), h = row & ((1 << lg) - 1);
         const uint32_t dst = smem_u32(s.q) + (c / 8) * kHalf + swz(row, (c % 8) * 16, 128);
@@ -141,25 +169,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     for (int i = tid; i < kWords; i += NT) ls.bits[i] = 0u;
     for (int i = tid; i < kMaxEntries; i += NT) s.mask[i] = 0ull;
     if (tid < 64) ls.late[tid] = 0u;
-    if (tid == 64) {
-        mbar_init(&s.k_full, 1);
-        mbar_init(&s.k_empty, 1);
-        mbar_init(&s.v_full, 1);
-        mbar_init(&s.v_empty, 1);
-        mbar_init(&s.s_full, 1);
-        mbar_init(&s.p_ready, 8);
-        mbar_init(&s.pv_done, 1);
-        mbar_init(&s.drain, 1);
-        fence_mbar_init();
-    }
     const int full = len / BK, npages = (len + BK - 1) / BK;  // complete pages, pages
     if (warp == kTmaWarp) {
-        if (lane == 0) {
-            prefetch_tmap(&tm_kp);
-            prefetch_tmap(&tm_vp);
-            if (r == 0 && ct == 0 && split == 0 && (len != a.cache_len[b] || nodes != a.n_nodes[b]))
-                raise_flag(a.status, MSA_DEV_BAD_BLOCK, 0xc01);
-        }
+        if (lane == 0 && r == 0 && ct == 0 && split == 0 && (len != a.cache_len[b] || nodes != a.n_nodes[b]))
+            raise_flag(a.status, MSA_DEV_BAD_BLOCK, 0xc01);
         unsigned long long anc[2];
         tree_ancestors(a, nodes, p0, p1, anc, 0xc02);
         int off[2];
@@ -181,7 +194,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
 #pragma unroll
     for (int x = 0; x < EPT; ++x) {
         const int nl = list_of(tid + x * NT);
-        pg[x] = 0;
         if (id[x] == -1 || nl >= mine) {
             id[x] = -1;
         } else if (id[x] < -1 || id[x] > ls.local[n0 + nl]) {
@@ -191,7 +203,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             if (id[x] >= full) atomicOr(&ls.late[nl], 1u << (id[x] - full));
             if (id[x] < npages) {
                 atomicOr(&ls.bits[id[x] >> 5], 1u << (id[x] & 31));
-                pg[x] = tree_page(a, b, id[x], 0xc04);
+                if ((unsigned)pg[x] >= (unsigned)a.num_pages) {
+                    raise_flag(a.status, MSA_DEV_BAD_BLOCK, 0xc04);
+                    pg[x] = 0;
+                }
             } else {
                 id[x] = -1;
             }
@@ -231,10 +246,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     __syncthreads();
     const int U = s.total;
     const int page_tiles = (U + TPT - 1) / TPT;
-    // tiles of this split: page tiles, then the drafted tokens' tile; none where the CTA has no nodes
-    const int tiles = mine > 0 ? page_tiles + 1 : 0;
-    const int t0 = tiles * split / a.splits, t1 = tiles * (split + 1) / a.splits;
-    const int e_lo = t0 * TPT, e_hi = min(U, t1 * TPT);
+    // tiles of this split (the first has tile 0, the drafted tokens; page tile i is tile i + 1)
+    const int tiles = page_tiles + 1;
+    const int t0 = (tiles * split + a.splits - 1) / a.splits, t1 = (tiles * (split + 1) + a.splits - 1) / a.splits;
+    const int e_lo = max(0, t0 - 1) * TPT, e_hi = min(U, max(0, t1 - 1) * TPT);
 #pragma unroll
     for (int x = 0; x < EPT; ++x) {
         if (id[x] < 0) continue;
@@ -245,7 +260,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     }
     // keys of the last page tile: the cache's last page, if chosen, holds len % block_k
     const int last_keys = (U - (page_tiles - 1) * TPT) * BK - (s.partial ? BK - len % BK : 0);
-    auto tile_keys = [&](int t) { return t < page_tiles - 1 ? kTile : t < page_tiles ? last_keys : nodes; };
+    auto tile_keys = [&](int t) { return t == 0 ? nodes : t < page_tiles ? kTile : last_keys; };
     cp_async_wait_all();
     fence_proxy_async();
     tc_fence_before();
@@ -261,12 +276,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         bool ok = true;
         for (; j < n_tiles; ++j) {
             const int t = t0 + j;
-            const bool drafted = t == page_tiles;
-            const int cnt = drafted ? 1 : min(TPT, U - t * TPT);
-            const uint32_t bytes = drafted ? 64u * D * 2 : (uint32_t)cnt * BK * D * 2;
+            if (t == 0) continue;  // under way since the start
+            const int e0 = (t - 1) * TPT, cnt = min(TPT, U - e0);
             int rows[TPT];
 #pragma unroll
-            for (int x = 0; x < TPT; ++x) rows[x] = x < cnt && !drafted ? s.page[t * TPT + x - e_lo] * BK : 0;
+            for (int x = 0; x < TPT; ++x) rows[x] = x < cnt ? s.page[e0 + x - e_lo] * BK : 0;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
                 uint64_t* fullb = kv ? &s.v_full : &s.k_full;
@@ -274,18 +288,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                 if (!ok) break;
                 if (leader) {
                     uint8_t* dst = kv ? s.v : s.k;
-                    mbar_arrive_expect_tx(fullb, bytes);
+                    mbar_arrive_expect_tx(fullb, (uint32_t)cnt * BK * D * 2);
 #pragma unroll
-                    for (int h = 0; h < D / 64; ++h) {
-                        if (drafted) {
-                            tma_load_4d(dst + h * kHalf, kv ? &tm_vd : &tm_kd, fullb, 64 * h, r, 0, b);
-                        } else {
+                    for (int h = 0; h < D / 64; ++h)
 #pragma unroll
-                            for (int x = 0; x < TPT; ++x)
-                                if (x < cnt)
-                                    tma_load_3d(dst + h * kHalf + x * BK * 128, kv ? &tm_vp : &tm_kp, fullb, 64 * h, r, rows[x]);
-                        }
-                    }
+                        for (int x = 0; x < TPT; ++x)
+                            if (x < cnt)
+                                tma_load_3d(dst + h * kHalf + x * BK * 128, kv ? &tm_vp : &tm_kp, fullb, 64 * h, r, rows[x]);
                 }
                 __syncwarp();
             }
@@ -358,14 +367,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         bool ok = true;
         for (int j = 0; ok && j < n_tiles; ++j) {
             const int t = t0 + j, keys = tile_keys(t);
-            const bool whole = t < page_tiles && keys == kTile;  // every column is a cached key
+            const bool whole = t > 0 && keys == kTile;  // every column is a cached key
             // this thread's two chunks of 32 columns: all-ones or zero words; in a tile that is not whole the columns
             // one by one
             uint32_t see[2];
-            if (t < page_tiles) {
+            if (t > 0) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int e = t * TPT + (2 * hf + c) / (BK / 32);
+                    const int e = (t - 1) * TPT + (2 * hf + c) / (BK / 32);
                     see[c] = (TPT == 1 || e < U) && (my_mask[2 * (e - e_lo)] & my_bit) ? 0xffffffffu : 0u;
                     if (!whole) {
                         const int left = keys - 64 * hf - 32 * c;  // keys in this chunk
@@ -522,44 +531,47 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             if (write && part) a.lse_part[split * n_rows + out_row(row)] = lse;
             if (write && !part && a.lse) a.lse[out_row(row)] = lse;
             if (!part || n_tiles > 0) {
-                const bool half = !part && a.out_bf16;
                 uint8_t* stage = s.q + warp * (32 * CW * 4);
-                const int lp = (half ? 1 : 2) + (CW == 64 ? 2 : 1), pieces = 1 << lp;  // 16-byte pieces of a row
-                const int sw = pieces - 1 < 7 ? pieces - 1 : 7;
+                auto store = [&](auto half_c, auto* base) {  // base: the output's row 0
+                    constexpr bool kHalfOut = decltype(half_c)::value;
+                    constexpr int LP = (kHalfOut ? 1 : 2) + (CW == 64 ? 2 : 1), P = 1 << LP;  // 16-byte pieces of a row
+                    constexpr int SW = P - 1 < 7 ? P - 1 : 7;
 #pragma unroll
-                for (int c = 0; c < CW / 16; ++c) {
-                    uint32_t o[16];
-                    if (n_tiles > 0) {
-                        tmem_ld16(tO + 16 * c, o);
-                        tmem_ld_wait();
-                        reg_fence(o);
+                    for (int c = 0; c < CW / 32; ++c) {
+                        uint32_t o[32];
+                        if (n_tiles > 0) {
+                            tmem_ld32(tO + 32 * c, o);
+                            tmem_ld_wait();
+                            reg_fence(o);
+                        }
+                        float f[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) f[e] = has ? __uint_as_float(o[e]) * inv : 0.f;
+#pragma unroll
+                        for (int e = 0; e < (kHalfOut ? 4 : 8); ++e) {
+                            uint4 val;
+                            if (kHalfOut)
+                                val = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
+                                                 pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+                            else
+                                val = make_uint4(__float_as_uint(f[4 * e]), __float_as_uint(f[4 * e + 1]),
+                                                 __float_as_uint(f[4 * e + 2]), __float_as_uint(f[4 * e + 3]));
+                            *reinterpret_cast<uint4*>(stage + lane * P * 16 + (((c * (kHalfOut ? 4 : 8) + e) ^ (lane & SW)) << 4)) = val;
+                        }
                     }
-                    float f[16];
+                    __syncwarp();
+                    constexpr int RP = 32 / P;  // rows a pass of the warp writes
+                    const int pc = lane & (P - 1);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = has ? __uint_as_float(o[e]) * inv : 0.f;
-                    if (half) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            *reinterpret_cast<uint4*>(stage + (lane << (lp + 4)) + (((2 * c + e) ^ (lane & sw)) << 4)) =
-                                make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
-                                           pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            *reinterpret_cast<float4*>(stage + (lane << (lp + 4)) + (((4 * c + e) ^ (lane & sw)) << 4)) =
-                                make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    for (int i = 0; i < 32 / RP; ++i) {
+                        const int rr = i * RP + lane / P, ri = (warp & 3) * 32 + rr;
+                        if (n0 + (ri >> lg) < a.T)
+                            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(base + out_row(ri) * D + hf * CW) + pc * 16) =
+                                *reinterpret_cast<const uint4*>(stage + rr * P * 16 + ((pc ^ (rr & SW)) << 4));
                     }
-                }
-                __syncwarp();
-                for (int i = lane; i < 32 << lp; i += 32) {
-                    const int rr = i >> lp, pc = i & (pieces - 1), ri = (warp & 3) * 32 + rr;
-                    if (n0 + (ri >> lg) >= a.T) break;
-                    const uint4 val = *reinterpret_cast<const uint4*>(stage + (rr << (lp + 4)) + ((pc ^ (rr & sw)) << 4));
-                    uint8_t* dst = half ? reinterpret_cast<uint8_t*>(a.out_bf16 + out_row(ri) * D + hf * CW)
-                                        : reinterpret_cast<uint8_t*>((part ? a.o_part + split * n_rows * D : a.out) +
-                                                                     out_row(ri) * D + hf * CW);
-                    *reinterpret_cast<uint4*>(dst + pc * 16) = val;
-                }
+                };
+                if (!part && a.out_bf16) store(std::true_type{}, a.out_bf16);
+                else store(std::false_type{}, part ? a.o_part + split * n_rows * D : a.out);
             }
         }
     }
