@@ -603,12 +603,29 @@ __global__ void __launch_bounds__(256) k_tree_combine(const __grid_constant__ Tr
     float acc[kPer];
 #pragma unroll
     for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
-    for (int p = 0; p < a.splits; ++p) {
-        const float wp = __shfl_sync(0xffffffffu, my_w, p);
-        if (wp == 0.f) continue;
-        const float* o = a.o_part + (p * n_rows + w) * D + lane * kPer;
+    // four parts under way at a time (one by one, the 18 parts of a single node took 2 us longer); a part of weight 0 is
+    // not read: it may never have been written
+    for (int p0 = 0; p0 < a.splits; p0 += 4) {
+        float f[4][kPer], wp[4];
 #pragma unroll
-        for (int x = 0; x < kPer; ++x) acc[x] = fmaf(wp, o[x], acc[x]);
+        for (int i = 0; i < 4; ++i) {
+            wp[i] = __shfl_sync(0xffffffffu, my_w, (p0 + i) & 31);  // (lanes behind the last split hold 0)
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) f[i][x] = 0.f;
+            if (wp[i] == 0.f) continue;
+            const float* o = a.o_part + ((p0 + i) * n_rows + w) * D + lane * kPer;
+            if (kPer == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(o);
+                f[i][0] = v.x, f[i][1] = v.y, f[i][kPer - 2] = v.z, f[i][kPer - 1] = v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(o);
+                f[i][0] = v.x, f[i][1] = v.y;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) acc[x] = fmaf(wp[i], f[i][x], acc[x]);
     }
     const float inv = z > 0.f || z != z ? 1.f / z : 0.f;
     if (a.out_bf16) {
