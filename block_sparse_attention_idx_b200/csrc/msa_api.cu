@@ -173,11 +173,11 @@ msa_status check_tree_sizes(const msa_dims* d, int T) {
 size_t ws_tree_index(const msa_dims* d, int T) {
     return kStatusBytes + tree_index_ws_bytes(d->B, d->N, d->H_kv, d->block_k, T);
 }
-int tree_splits(const msa_dims* d, int T) {
-    return tree_attn_splits(d->B, T, d->H_q, d->H_kv, d->block_k, d->topk, num_sms());
-}
 size_t ws_tree_attn(const msa_dims* d, int T) {
-    return kStatusBytes + tree_attn_ws_bytes(d->B, T, d->H_q, d->d, tree_splits(d, T));
+    TreeArgs a{};
+    a.B = d->B; a.T = T; a.H_q = d->H_q; a.H_kv = d->H_kv; a.d = d->d; a.block_k = d->block_k; a.topk = d->topk;
+    tree_attn_plan(&a, num_sms());
+    return kStatusBytes + tree_attn_ws_bytes(a);
 }
 TreeArgs tree_args(const msa_dims* d, const msa_pages* p, const msa_tree* t, DevStatus* status) {
     TreeArgs a{};
@@ -676,13 +676,8 @@ static msa_status tree_attn(const msa_dims* d, const msa_pages* p, const msa_tre
     if (status_init(status, st) != cudaSuccess) return MSA_ERR_CUDA;
     TreeArgs a = tree_args(d, p, t, status);
     a.blocks = blocks;
-    a.splits = tree_splits(d, t->T);
-    if (a.splits > 1) {
-        Carver cv{static_cast<uint8_t*>(ws) + kStatusBytes};
-        const size_t rows = (size_t)a.splits * d->B * t->T * d->H_q;
-        a.lse_part = reinterpret_cast<float*>(cv.take(rows * 4));
-        a.o_part = reinterpret_cast<float*>(cv.take(rows * d->d * 4));
-    }
+    tree_attn_plan(&a, num_sms());
+    tree_attn_carve(&a, static_cast<uint8_t*>(ws) + kStatusBytes);
     a.out = out;
     a.out_bf16 = out_bf16;
     a.lse = lse;

@@ -241,9 +241,13 @@ struct TreeArgs {
     const int32_t* blocks;
     int lg_g;                        // log2(H_q / H_kv)
     int k1_inv;                      // floor(2^16 / (topk + 1)) + 1: e / (topk + 1) = e * k1_inv >> 16 for e < 3800
-    int splits;                      // key splits of the attention
-    float* o_part;                   // [splits, B, T, H_q, d] normalised partial outputs (splits > 1)
-    float* lse_part;                 // [splits, B, T, H_q]
+    int slots;                       // attention CTAs that run at once
+    int max_splits;                  // CTAs that may share one item's keys
+    int part_rows;                   // rows of an item: 128, or all of a sequence's rows of a group
+    float* o_part;                   // [slots, part_rows, d] normalised partial outputs
+    float* lse_part;                 // [slots, part_rows]
+    int4* split_items;               // [slots / 2] sequence, group and node tile of an item split over CTAs
+    int2* split_count;               // number of them, CTAs of each
     float* out;                      // [B, T, H_q, d], or null when out_bf16 is set
     __nv_bfloat16* out_bf16;
     float* lse;                      // [B, T, H_q] or null
@@ -253,8 +257,9 @@ size_t tree_index_ws_bytes(int B, int N, int H_kv, int block_k, int T);
 void tree_index_carve(TreeArgs* a, void* base);
 cudaError_t run_tree_index(const TreeArgs& a, const void* q_idx, const void* k_idx, const void* k_idx_pool, int num_sms,
                            cudaStream_t st);
-int tree_attn_splits(int B, int T, int H_q, int H_kv, int block_k, int topk, int num_sms);
-size_t tree_attn_ws_bytes(int B, int T, int H_q, int d, int splits);
+void tree_attn_plan(TreeArgs* a, int num_sms);  // fills slots and max_splits
+size_t tree_attn_ws_bytes(const TreeArgs& a);   // of a planned call, behind the status word
+void tree_attn_carve(TreeArgs* a, void* base);
 cudaError_t run_tree_attn(const TreeArgs& a, const void* q, const void* k, const void* v, const void* k_pool,
                           const void* v_pool, cudaStream_t st);
 

@@ -17,8 +17,16 @@
 //
 // A CTA is a chain: S, exponentials, PV, next S. Two CTAs share an SM (256 TMEM columns, 113 KB and 96 registers a
 // thread each), so that one's products, loads, list building and output run under the other's exponentials. K and V
-// have one buffer each: K of the next tile arrives during this tile's exponentials, V during the next tile's. Where the
-// CTAs do not fill the device the union is split over `splits` CTAs and merged by k_tree_combine.
+// have one buffer each: K of the next tile arrives during this tile's exponentials, V during the next tile's. The last
+// wave of CTAs, if it would fill at most half of the device, splits its unions over several CTAs, merged by
+// k_tree_combine: 64 nodes over 16 x 65536 tokens (408 items of 128 rows, 30 tiles each; 64 query heads in 4 groups,
+// d = 128) take 132 us instead of 144, and a few nodes of a long tree take what they would take alone.
+//
+// Bound, 64 nodes: the chain. A tile takes 3700 cycles, 2030 of them the exponentials and what is around them (1024 on
+// the MUFU, which both CTAs share), 1650 from P to the next S (1024 of products: 128 x 128 x 16 take 64 cycles with both
+// operands in shared memory); the tensor pipe is busy 32 % of the time, the MUFU 31 %. At 8 nodes a sequence (256 CTAs of
+// 6 tiles: 40 us with the merge) it waits for pages that nobody has read before (2300 cycles a tile for V), and list
+// building and output cost 9 us of a CTA's 28.
 #include <type_traits>
 
 #include "msa_tree.cuh"
@@ -67,6 +75,80 @@ __device__ __forceinline__ float max3n(float a, float b, float c) {
     return m;
 }
 
+// An item is 128 rows: the nodes ct * 128/G .. of sequence b, group r. Items without a node that exists are left out
+// (unless a sequence has only one item per group). The device runs `slots` CTAs at once, so the items' last, part-filled
+// wave is the one whose length counts: its `rem` items are split over `splits` CTAs each, as many as the slots hold.
+struct TreeUnit {
+    int b, r, ct;
+    int split, splits;
+    int part;  // of the partial outputs, where splits > 1: split i of the j-th split item has part i * (split items) + j
+};
+__device__ __forceinline__ int tree_items(const TreeArgs& a, int b) {  // per group of sequence b
+    const int sh = 7 - a.lg_g;
+    return b >= a.B ? 0 : a.T <= (kRows >> a.lg_g) ? 1 : (tree_nodes(a, b) + (1 << sh) - 1) >> sh;
+}
+// Called by whole warps. What CTA `unit` does; false if nothing. Items are ordered by sequence, group and node:
+// neighbours share pages. count: the split items and their CTAs.
+__device__ __forceinline__ bool tree_unit(const TreeArgs& a, int unit, TreeUnit* u, int2* count) {
+    const int lane = threadIdx.x & 31;
+    const bool even = a.T <= (kRows >> a.lg_g);  // one item per sequence and group
+    int live = a.B;
+    if (!even) {
+        live = 0;
+        for (int b = lane; b < a.B; b += 32) live += tree_items(a, b);
+        live = __reduce_add_sync(0xffffffffu, live);
+    }
+    live *= a.H_kv;
+    const int base = live < a.slots ? 0 : live / a.slots * a.slots, rem = live - base;
+    const int splits = rem > 0 ? max(1, min(a.max_splits, a.slots / rem)) : 1;
+    *count = make_int2(rem, splits);
+    int item = unit;
+    u->split = 0, u->splits = 1, u->part = 0;
+    if (unit >= base) {
+        if (unit - base >= rem * splits) return false;
+        u->part = unit - base, u->splits = splits, u->split = u->part / rem, item = unit - u->split * rem;
+    }
+    if (even) {
+        u->b = item / a.H_kv, u->r = item - u->b * a.H_kv, u->ct = 0;
+        return true;
+    }
+    int before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int n = tree_items(a, b0 + lane), mine = n * a.H_kv;
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += t;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + incl > item);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            const int at = item - before - __shfl_sync(0xffffffffu, incl - mine, l), per = __shfl_sync(0xffffffffu, n, l);
+            u->b = b0 + l, u->r = at / per, u->ct = at - u->r * per;
+            return true;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return false;
+}
+
+// Zeros and LSE -inf for the rows of nodes n0 .. that lie in T.
+__device__ __forceinline__ void tree_zero_rows(const TreeArgs& a, int b, int r, int n0) {
+    const int lg = a.lg_g, rows = min(kRows, (a.T - n0) << lg), pieces = a.d / 8;
+    auto out_row = [&](int i) { return ((int64_t)b * a.T + n0 + (i >> lg)) * a.H_q + (r << lg) + (i & ((1 << lg) - 1)); };
+    for (int i = threadIdx.x; a.lse && i < rows; i += blockDim.x) a.lse[out_row(i)] = -INFINITY;
+    for (int i = threadIdx.x; i < rows * pieces; i += blockDim.x) {
+        const int64_t o = out_row(i / pieces) * a.d + (i % pieces) * 8;
+        if (a.out_bf16) {
+            *reinterpret_cast<uint4*>(a.out_bf16 + o) = make_uint4(0, 0, 0, 0);
+        } else {
+            *reinterpret_cast<uint4*>(a.out + o) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(a.out + o + 4) = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
 template <int D, int BK>
 __global__ void __launch_bounds__(kAttnThreads, 2)
     k_tree_attn(const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
@@ -86,10 +168,27 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     const int lg = a.lg_g, K1 = a.topk + 1;     // G = 2^lg heads per group
     const int per_cta = kRows >> lg;            // nodes
     auto list_of = [&](int e) { return (e * a.k1_inv) >> 16; };  // e / K1
-    const int n_ct = (a.T + per_cta - 1) / per_cta;
-    const int ct = blockIdx.x % n_ct, br = blockIdx.x / n_ct, r = br % a.H_kv, b = br / a.H_kv;
-    const int split = blockIdx.y, n0 = ct * per_cta;
-    const int64_t n_rows = (int64_t)a.B * a.T * a.H_q;
+    if (a.T > per_cta) {  // items without a node: CTA i writes the i-th of all, if it is one
+        const int n_ct = (a.T + per_cta - 1) / per_cta, i = blockIdx.x;
+        const int zc = i % n_ct, zr = i / n_ct % a.H_kv, zb = i / n_ct / a.H_kv;
+        if (zb < a.B && zc * per_cta >= tree_nodes(a, zb)) {
+            tree_zero_rows(a, zb, zr, zc * per_cta);
+            if (tid == 0 && zr == 0 && zc == 0 && (tree_len(a, zb) != a.cache_len[zb] || a.n_nodes[zb] != 0))
+                raise_flag(a.status, MSA_DEV_BAD_BLOCK, 0xc01);
+        }
+    }
+    TreeUnit u;
+    int2 count;
+    const bool live_cta = tree_unit(a, blockIdx.x, &u, &count);
+    if (tid == 0) {  // for the merge
+        if (blockIdx.x == 0) *a.split_count = count;
+        if (live_cta && u.splits > 1 && u.split == 0) a.split_items[u.part] = make_int4(u.b, u.r, u.ct, 0);
+    }
+    if (!live_cta) {
+        pdl_trigger();
+        return;
+    }
+    const int b = u.b, r = u.r, ct = u.ct, split = u.split, n0 = ct * per_cta;
 
     // ------------------------------------------------------------------ the union of the CTA's lists
     // Loads that depend on nothing go first: the lists (kept in registers), the parents, Q. Rows of nodes that
@@ -112,24 +211,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         p1 = load_parent(a, b, lane + 32);
     }
     const int len = tree_len(a, b), nodes = tree_nodes(a, b);
-    if (n0 >= nodes) {  // none of the CTA's nodes exists: zeros (its partial outputs are not read) and LSE -inf
-        if (tid == 0 && r == 0 && ct == 0 && split == 0 && (len != a.cache_len[b] || nodes != a.n_nodes[b]))
+    if (n0 >= nodes) {  // a sequence without nodes: zeros (its partial outputs are not read) and LSE -inf
+        if (tid == 0 && r == 0 && split == 0 && (len != a.cache_len[b] || nodes != a.n_nodes[b]))
             raise_flag(a.status, MSA_DEV_BAD_BLOCK, 0xc01);
-        const int rows = min(kRows, (a.T - n0) << lg);
-        auto out_row = [&](int i) { return ((int64_t)b * a.T + n0 + (i >> lg)) * a.H_q + (r << lg) + (i & ((1 << lg) - 1)); };
-        for (int i = tid; i < rows; i += NT) {
-            if (a.splits > 1) a.lse_part[split * n_rows + out_row(i)] = -INFINITY;
-            else if (a.lse) a.lse[out_row(i)] = -INFINITY;
-        }
-        for (int i = tid; a.splits == 1 && i < rows * (D / 8); i += NT) {
-            const int64_t o = out_row(i / (D / 8)) * D + (i % (D / 8)) * 8;
-            if (a.out_bf16) {
-                *reinterpret_cast<uint4*>(a.out_bf16 + o) = make_uint4(0, 0, 0, 0);
-            } else {
-                *reinterpret_cast<uint4*>(a.out + o) = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4*>(a.out + o + 4) = make_uint4(0, 0, 0, 0);
-            }
-        }
+        if (u.splits == 1) tree_zero_rows(a, b, r, n0);
+        else if (tid < a.part_rows) a.lse_part[u.part * a.part_rows + tid] = -INFINITY;
         pdl_trigger();
         return;
     }
@@ -248,7 +334,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     const int page_tiles = (U + TPT - 1) / TPT;
     // tiles of this split (the first has tile 0, the drafted tokens; page tile i is tile i + 1)
     const int tiles = page_tiles + 1;
-    const int t0 = (tiles * split + a.splits - 1) / a.splits, t1 = (tiles * (split + 1) + a.splits - 1) / a.splits;
+    const int t0 = (tiles * split + u.splits - 1) / u.splits, t1 = (tiles * (split + 1) + u.splits - 1) / u.splits;
     const int e_lo = max(0, t0 - 1) * TPT, e_hi = min(U, max(0, t1 - 1) * TPT);
 #pragma unroll
     for (int x = 0; x < EPT; ++x) {
@@ -505,8 +591,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             if (lane == 0) mbar_arrive(&s.p_ready);
         }
         // -------------------------------------------------------------------- outputs
-        // Through shared memory (Q and K are no longer read: the last S was issued before the last PV), so that a warp writes whole rows: 32 rows of 16-byte pieces straight from the lanes took 4 us at the
-        // end of every CTA.
+        // Through shared memory (Q and K are no longer read: the last S was issued before the last PV), so that a warp
+        // writes whole rows: 32 rows of 16-byte pieces straight from the lanes took 4 us at the end of every CTA.
         if (ok && n_tiles > 0) {
             bool done = false;
             for (int i = 0; i < 32 && !done; ++i) done = mbar_try_wait(&s.pv_done, 0);  // before the timed wait's loads
@@ -519,7 +605,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         bar_sync_named(pair_bar, 64);
         if (ok) {
             const float l = s.row_sum[0][row] + s.row_sum[1][row];
-            const bool part = a.splits > 1;
+            const bool part = u.splits > 1;
             const bool has = l > 0.f || l != l;  // a NaN sum stays NaN
             const float inv = has ? 1.f / l : 0.f;
             const float lse = has ? (mref + log2f(l)) * 0.6931471805599453f : -INFINITY;
@@ -528,11 +614,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                 return ((int64_t)b * a.T + n0 + (i >> lg)) * a.H_q + (r << lg) + (i & ((1 << lg) - 1));
             };
             const bool write = hf == 0 && n0 + nl < a.T;
-            if (write && part) a.lse_part[split * n_rows + out_row(row)] = lse;
+            if (hf == 0 && part && row < a.part_rows) a.lse_part[u.part * a.part_rows + row] = lse;
             if (write && !part && a.lse) a.lse[out_row(row)] = lse;
             if (!part || n_tiles > 0) {
                 uint8_t* stage = s.q + warp * (32 * CW * 4);
-                auto store = [&](auto half_c, auto* base) {  // base: the output's row 0
+                auto store = [&](auto half_c, auto* base, auto at) {  // row i goes to row at(i) of base
                     constexpr bool kHalfOut = decltype(half_c)::value;
                     constexpr int LP = (kHalfOut ? 1 : 2) + (CW == 64 ? 2 : 1), P = 1 << LP;  // 16-byte pieces of a row
                     constexpr int SW = P - 1 < 7 ? P - 1 : 7;
@@ -566,12 +652,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                     for (int i = 0; i < 32 / RP; ++i) {
                         const int rr = i * RP + lane / P, ri = (warp & 3) * 32 + rr;
                         if (n0 + (ri >> lg) < a.T)
-                            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(base + out_row(ri) * D + hf * CW) + pc * 16) =
+                            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(base + at(ri) * D + hf * CW) + pc * 16) =
                                 *reinterpret_cast<const uint4*>(stage + rr * P * 16 + ((pc ^ (rr & SW)) << 4));
                     }
                 };
-                if (!part && a.out_bf16) store(std::true_type{}, a.out_bf16);
-                else store(std::false_type{}, part ? a.o_part + split * n_rows * D : a.out);
+                if (part) store(std::false_type{}, a.o_part + (int64_t)u.part * a.part_rows * D, [](int i) { return i; });
+                else if (a.out_bf16) store(std::true_type{}, a.out_bf16, out_row);
+                else store(std::false_type{}, a.out, out_row);
             }
         }
     }
@@ -582,16 +669,20 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     pdl_trigger();
 }
 
-// One warp per (node, head): log-sum-exp merge of the splits' partials (at most 32). A split that saw no
-// token of the row has LSE = -inf and an output that is not read.
+// Items split over CTAs: log-sum-exp merge of their parts (at most 32), one warp per row (blockIdx.y: the item). A part
+// that saw no token of the row has LSE = -inf and an output that is not read.
 template <int D>
 __global__ void __launch_bounds__(256) k_tree_combine(const __grid_constant__ TreeArgs a) {
-    const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31;
-    const int64_t n_rows = (int64_t)a.B * a.T * a.H_q;
-    if (w >= n_rows) return;
+    const int row = blockIdx.x * 8 + warp_id(), lane = threadIdx.x & 31, y = blockIdx.y;
     pdl_wait();
-    const float my_l = lane < a.splits ? a.lse_part[lane * n_rows + w] : -INFINITY;
+    const int2 count = *a.split_count;
+    const int4 it = a.split_items[y];
+    const int splits = count.y, step = count.x * a.part_rows, first = y * a.part_rows + row;  // the row in part p: first + p * step
+    if (splits == 1 || y >= count.x || row >= a.part_rows) return;
+    const float my_l = lane < splits ? a.lse_part[first + lane * step] : -INFINITY;
+    const int node = it.z * (kRows >> a.lg_g) + (row >> a.lg_g);
+    if (node >= a.T) return;
+    const int64_t w = ((int64_t)it.x * a.T + node) * a.H_q + (it.y << a.lg_g) + (row & ((1 << a.lg_g) - 1));
     float mx = my_l;
 #pragma unroll
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -603,17 +694,16 @@ __global__ void __launch_bounds__(256) k_tree_combine(const __grid_constant__ Tr
     float acc[kPer];
 #pragma unroll
     for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
-    // four parts under way at a time (one by one, the 18 parts of a single node took 2 us longer); a part of weight 0 is
-    // not read: it may never have been written
-    for (int p0 = 0; p0 < a.splits; p0 += 4) {
-        float f[4][kPer], wp[4];
+    // Six parts under way at a time, without branches (one by one the 18 parts of a single node took 4 us longer). A part
+    // of weight 0 may never have been written: what it holds is dropped.
+    for (int p0 = 0; p0 < splits; p0 += 6) {
+        float f[6][kPer], wp[6];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            wp[i] = __shfl_sync(0xffffffffu, my_w, (p0 + i) & 31);  // (lanes behind the last split hold 0)
-#pragma unroll
-            for (int x = 0; x < kPer; ++x) f[i][x] = 0.f;
-            if (wp[i] == 0.f) continue;
-            const float* o = a.o_part + ((p0 + i) * n_rows + w) * D + lane * kPer;
+        for (int i = 0; i < 6; ++i) {
+            const int p = min(p0 + i, splits - 1);
+            wp[i] = __shfl_sync(0xffffffffu, my_w, p);
+            if (p0 + i >= splits) wp[i] = 0.f;
+            const float* o = a.o_part + (int64_t)(first + p * step) * D + lane * kPer;
             if (kPer == 4) {
                 const float4 v = *reinterpret_cast<const float4*>(o);
                 f[i][0] = v.x, f[i][1] = v.y, f[i][kPer - 2] = v.z, f[i][kPer - 1] = v.w;
@@ -623,9 +713,9 @@ __global__ void __launch_bounds__(256) k_tree_combine(const __grid_constant__ Tr
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 6; ++i)
 #pragma unroll
-            for (int x = 0; x < kPer; ++x) acc[x] = fmaf(wp[i], f[i][x], acc[x]);
+            for (int x = 0; x < kPer; ++x) acc[x] = fmaf(wp[i], wp[i] == 0.f ? 0.f : f[i][x], acc[x]);
     }
     const float inv = z > 0.f || z != z ? 1.f / z : 0.f;
     if (a.out_bf16) {
@@ -648,16 +738,26 @@ int tree_ctas(int B, int T, int H_q, int H_kv) {
 
 }  // namespace
 
-// Splits of the key walk: none once the CTAs fill the device; else as many as fill it, at most one per tile
-// of a single node's list.
-int tree_attn_splits(int B, int T, int H_q, int H_kv, int block_k, int topk, int num_sms) {
-    const int tpt = kTile / block_k, tiles = (topk + 1 + tpt - 1) / tpt + 1;
-    return std::max(1, std::min({tiles, 2 * num_sms / tree_ctas(B, T, H_q, H_kv), 32}));
+// (at most one split per tile of a single node's list)
+void tree_attn_plan(TreeArgs* a, int num_sms) {
+    const int tpt = kTile / a->block_k;
+    a->slots = 2 * num_sms;
+    a->max_splits = std::min((a->topk + tpt) / tpt + 1, 32);
+    a->part_rows = std::min(kRows, a->T * (a->H_q / a->H_kv));
 }
-size_t tree_attn_ws_bytes(int B, int T, int H_q, int d, int splits) {
-    if (splits <= 1) return 0;
-    const size_t rows = (size_t)splits * B * T * H_q;
-    return ((rows * 4 + 255) & ~size_t(255)) + rows * d * 4;
+// Partial outputs that may be under way: of `slots` CTAs, or fewer where there are few items.
+static size_t tree_parts(const TreeArgs& a) {
+    return std::min<size_t>(a.slots, (size_t)tree_ctas(a.B, a.T, a.H_q, a.H_kv) * a.max_splits);
+}
+size_t tree_attn_ws_bytes(const TreeArgs& a) {
+    return ((tree_parts(a) * a.part_rows * (a.d + 1) * 4 + 15) & ~size_t(15)) + (a.slots / 2) * sizeof(int4) + 16;
+}
+void tree_attn_carve(TreeArgs* a, void* base) {
+    a->o_part = static_cast<float*>(base);
+    const size_t rows = tree_parts(*a) * a->part_rows;
+    a->lse_part = a->o_part + rows * a->d;
+    a->split_items = reinterpret_cast<int4*>(static_cast<uint8_t*>(base) + ((rows * (a->d + 1) * 4 + 15) & ~size_t(15)));
+    a->split_count = reinterpret_cast<int2*>(a->split_items + a->slots / 2);
 }
 
 cudaError_t run_tree_attn(const TreeArgs& a, const void* q, const void* k, const void* v, const void* k_pool,
@@ -672,7 +772,8 @@ cudaError_t run_tree_attn(const TreeArgs& a, const void* q, const void* k, const
         !make_tmap_3d(&vp, v_pool, a.d, a.H_kv, slots, a.d * es, row, 64, 1, a.block_k, 128) ||
         !make_tmap_4d(&kd, k, dims, strides, box, 128) || !make_tmap_4d(&vd, v, dims, strides, box, 128))
         return cudaErrorInvalidValue;
-    const dim3 grid(tree_ctas(a.B, a.T, a.H_q, a.H_kv), a.splits);
+    const int items = tree_ctas(a.B, a.T, a.H_q, a.H_kv), parts = (int)tree_parts(a);
+    const dim3 grid(items / a.slots * a.slots + (items % a.slots ? parts : 0));  // enough for any number of live items
     const auto* qb = static_cast<const __nv_bfloat16*>(q);
     auto pick = [&](auto d_c, auto bk_c) -> cudaError_t {
         constexpr int D = decltype(d_c)::value, BK = decltype(bk_c)::value;
@@ -694,10 +795,9 @@ cudaError_t run_tree_attn(const TreeArgs& a, const void* q, const void* k, const
         else
             e = a.block_k == 128 ? pick(I64{}, I128{}) : a.block_k == 64 ? pick(I64{}, I64{}) : pick(I64{}, I32{});
     }
-    if (e != cudaSuccess || a.splits == 1) return e;
+    if (e != cudaSuccess) return e;
     ProfScope ps("tree_combine", st);
-    const int64_t rows = (int64_t)a.B * a.T * a.H_q;
-    const dim3 cgrid((unsigned)((rows + 7) / 8));
+    const dim3 cgrid((a.part_rows + 7) / 8, std::min(items, a.slots / 2));
     return a.d == 128 ? launch_pdl(k_tree_combine<128>, cgrid, dim3(256), 0, st, a)
                       : launch_pdl(k_tree_combine<64>, cgrid, dim3(256), 0, st, a);
 }

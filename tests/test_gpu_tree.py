@@ -340,6 +340,27 @@ def test_many_sequences_some_without_a_cache_or_nodes():
     _run(c)
 
 
+@pytest.mark.parametrize("nodes", ["all", "ragged", "few", "one"])
+def test_more_rows_than_the_device_runs_at_once(nodes):
+    """Up to 400 tiles of 128 rows (8 nodes each): full waves of CTAs, a split last wave, sequences without a node,
+    tiles without a node."""
+    g = torch.Generator().manual_seed(8)
+    B, T = 67, 20
+    nn = {"all": [T] * B, "ragged": torch.randint(0, T + 1, (B,), generator=g).tolist(), "one": [0] * (B - 1) + [T],
+          "few": [20 if b % 9 == 4 else b % 2 for b in range(B)]}[nodes]
+    lens = torch.randint(0, 400, (B,), generator=g).tolist()
+    c = Case(lens, T, H_q=32, H_kv=2, d=64, di=32, bk=32, topk=4, n_nodes=nn, seed=22)
+    blocks = c.select()
+    out, lse = c.attend(blocks, want_lse=True)
+    c.check_attention(blocks, out, lse, nodes=[0, 7, 8, 19])
+    out2, lse2 = c.attend(blocks, want_lse=True)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    b16, _ = c.attend(blocks, out_dtype=torch.bfloat16, want_lse=True)
+    assert torch.equal(b16, out.to(torch.bfloat16))
+    dead = torch.arange(T, device=DEV)[None] >= c.n_nodes[:, None]
+    assert (out[dead] == 0).all() and torch.isneginf(lse[dead]).all()
+
+
 @pytest.mark.parametrize("bk,L", [(32, 262144), (128, 262143), (64, 140001)])
 def test_largest_block_counts(bk, L):
     """Up to the 8192 blocks of a sequence: every Top-k variant, lists spread over the whole page table."""

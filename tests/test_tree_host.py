@@ -125,7 +125,9 @@ def test_tree_workspace_sizes():
     # block maxima of every (node, group) row dominate the selection's
     n = msa.msa_tree_workspace_size(msa.MSA_OP_TREE_INDEX_TOPK, d, 16)
     assert 16 * 16 * 4 * 2048 * 4 <= n < 1.1 * 16 * 16 * 4 * 2048 * 4
-    assert msa.msa_tree_workspace_size(msa.MSA_OP_TREE_ATTN, d, 64) == 256  # the CTAs fill the device: no splits
+    # partial outputs of at most two CTAs an SM, whatever the batch
+    big = dims(B=64, N=262144, H_q=64, H_kv=4, d=128, d_idx=64, block_k=128, topk=16)
+    assert msa.msa_tree_workspace_size(msa.MSA_OP_TREE_ATTN, d, 64) == msa.msa_tree_workspace_size(msa.MSA_OP_TREE_ATTN, big, 64)
     assert msa.msa_tree_workspace_size(msa.MSA_OP_TREE_ATTN, dims(B=1), 1) > 256
     for op, T in ((msa.MSA_OP_DECODE, 4), (msa.MSA_OP_TREE_ATTN, 0)):
         with pytest.raises(msa.MsaError):
