@@ -131,19 +131,26 @@ class PagedCache:
         need += sum(min(k, self._refs[p] - 1) for p, k in shared.items())
         if need > len(self._free):
             raise ValueError(f"{need} pages needed, {len(self._free)} free")
-        src, dst = [], []
+        copies, owners = [], {}  # (sequence, page) to copy; owners that a shared page has left
         for s, c in zip(seqs, counts):
             pages, n = self._seqs[s]
-            last = n // bk
-            if c and n % bk and self._refs[pages[last]] > 1:
-                src.append(pages[last])
-                dst.append(self._take())
-                self._refs[pages[last]] -= 1
-                pages[last] = dst[-1]
+            if c and n % bk:
+                p = pages[n // bk]
+                owners.setdefault(p, self._refs[p])
+                if owners[p] > 1:
+                    copies.append((s, p))
+                    owners[p] -= 1
+        if copies:  # before anything changes: the call may raise
+            src, dst = [p for _, p in copies], self._free[:-len(copies) - 1:-1]
+            msa.msa_cache_copy_pages(self.dims, src, dst, self.k_pool, self.v_pool, self.k_idx_pool, stream=stream)
+        for s, p in copies:
+            pages, n = self._seqs[s]
+            pages[n // bk] = self._take()
+            self._refs[p] -= 1
+        for s, c in zip(seqs, counts):
+            pages, n = self._seqs[s]
             while len(pages) * bk < n + c:
                 pages.append(self._take())
-        if src:
-            msa.msa_cache_copy_pages(self.dims, src, dst, self.k_pool, self.v_pool, self.k_idx_pool, stream=stream)
 
     def append(self, seqs, k, v, k_idx, counts=None, rows=None, stream=None) -> None:
         """Writes counts[i] new tokens (default: all T) behind sequence seqs[i]: the first rows of k, v
@@ -167,13 +174,14 @@ class PagedCache:
         if not any(counts):
             return
         dev = self.k_pool.device
-        n_new = torch.tensor(counts, dtype=torch.int32).to(dev)
-        row_t = None
-        if rows is not None:
-            width = max(counts)
-            row_t = torch.tensor([r + [0] * (width - len(r)) for r in rows], dtype=torch.int32).to(dev)
-        msa.msa_cache_append(self.dims_for(len(seqs)), self.pages(seqs), k, v, k_idx, self.k_pool, self.v_pool,
-                             self.k_idx_pool, n_new, rows=row_t, stream=stream)
+        with msa._on(stream):  # the index tensors belong to the stream that reads them
+            n_new = torch.tensor(counts, dtype=torch.int32).to(dev)
+            row_t = None
+            if rows is not None:
+                width = max(counts)
+                row_t = torch.tensor([r + [0] * (width - len(r)) for r in rows], dtype=torch.int32).to(dev)
+            msa.msa_cache_append(self.dims_for(len(seqs)), self.pages(seqs), k, v, k_idx, self.k_pool, self.v_pool,
+                                 self.k_idx_pool, n_new, rows=row_t, stream=stream)
         for s, c in zip(seqs, counts):
             self._seqs[s][1] += c
 
@@ -184,12 +192,12 @@ class PagedCache:
         holes = sorted(p for p in self._free if p < used)
         high = [p for p in range(used, self.num_pages) if self._refs[p]]
         move = dict(zip(high, holes))
+        if move:  # before anything changes: the call may raise
+            msa.msa_cache_copy_pages(self.dims, list(move), list(move.values()), self.k_pool, self.v_pool, self.k_idx_pool,
+                                     stream=stream)
         for s in self._seqs.values():
             s[0] = [move.get(p, p) for p in s[0]]
         for a, b in move.items():
             self._refs[b], self._refs[a] = self._refs[a], 0
         self._free = list(range(self.num_pages - 1, used - 1, -1))
-        if move:
-            msa.msa_cache_copy_pages(self.dims, list(move), list(move.values()), self.k_pool, self.v_pool, self.k_idx_pool,
-                                     stream=stream)
         return used

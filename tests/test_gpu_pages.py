@@ -202,3 +202,32 @@ def test_paged_cache_forks_and_compaction_on_the_device():
     check()
     grow([b, a], 33)
     check()
+
+
+def test_paged_cache_on_another_stream():
+    """The index tensors of an append on a side stream stay intact while it waits there, whatever the current stream
+    allocates and writes meanwhile."""
+    from block_sparse_attention_idx_b200.pages import PagedCache
+
+    c = PagedCache(msa.MsaDims(1, 256, 2, 2, 64, 32, 32, 2), 16)
+    for p in (c.k_pool, c.v_pool, c.k_idx_pool):
+        p.zero_()
+    g = torch.Generator(device=DEV).manual_seed(5)
+    k, v, ki = _bf(g, 2, 9, 2, 64), _bf(g, 2, 9, 2, 64), _bf(g, 2, 9, 32)
+    side, here, seqs, rows = torch.cuda.Stream(), torch.cuda.Stream(), [c.new(), c.new()], [[0, 3, 8], [1, 2]]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(here):
+        c.append([c.new(), c.new()], k, v, ki, rows=rows)  # (the kernels are loaded)
+        torch.zeros(4, dtype=I32, device=DEV)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)
+        c.append(seqs, k, v, ki, rows=rows, stream=side)
+        held = [torch.zeros(4, dtype=I32, device=DEV) for _ in range(16)]  # may take what is free for reuse here
+    torch.cuda.synchronize()
+    assert len(held) == 16
+    for b, s in enumerate(seqs):
+        page = c.page_list(s)[0]
+        assert torch.equal(c.k_pool[page, :len(rows[b])], k[b, rows[b]])
+        assert torch.equal(c.v_pool[page, :len(rows[b])], v[b, rows[b]])
+        assert torch.equal(c.k_idx_pool[page, :len(rows[b])], ki[b, rows[b]])

@@ -148,6 +148,27 @@ def test_errors_change_nothing(cache):
         _consistent(c)
 
 
+def test_a_copy_that_cannot_start_changes_nothing(cache, monkeypatch):
+    c = cache()
+    a, gone = c.new(), c.new()
+    k, v, ki = _tokens(1, 40, [list(range(40))])
+    c.append([gone], k, v, ki)
+    c.append([a], k, v, ki)
+    f = c.fork(a)
+    c.free(gone)
+    before = ([list(c._refs), list(c._free)], {s: c.page_list(s) for s in (a, f)})
+
+    def refuse(*args, **kw):
+        raise ValueError("another device's stream")
+
+    monkeypatch.setattr(msa, "msa_cache_copy_pages", refuse)
+    for call in (lambda: c.append([f], k, v, ki), lambda: c.reserve([a, f], [1, 1]), c.compact):
+        with pytest.raises(ValueError, match="another device"):
+            call()
+        assert before == ([list(c._refs), list(c._free)], {s: c.page_list(s) for s in (a, f)})
+        assert _read(c, a) == _read(c, f) == list(range(40))
+
+
 def test_page_table_and_lengths(cache):
     c = cache(N=100)
     a, b = c.new(), c.new()
