@@ -11,9 +11,9 @@
 // HBM-bound: every element is read and written once. A CTA takes one token's heads of all tensors as a flat list of
 // tasks (2V elements of a head, V pairs of one or two 16-byte loads each); a thread issues its first loads, works out
 // its share of the tables while they fly, then rotates. Resident warps are what covers the loads' latency: 16-bit
-// inputs run best in small CTAs of 40 registers (32768 tokens of 64 + 4 heads of 128 and 4 + 1 of 64 dims: 200 us,
-// 0.90 of the copy rate; 318 us with 90 registers and three tasks in flight, 299 us with a warp per token and
-// tensor), 32-bit ones, twice the bytes a task, with 64 registers (8191 tokens: 105 us; 153 us with 40).
+// inputs run best in small CTAs of 40 registers (32768 tokens of 64 + 4 heads of 128 and 4 + 1 of 64 dims: 194 us,
+// 0.93 of the copy rate; 198 us with 128 threads instead of 96, 253 us with 32 registers, 318 us with 90 and three
+// tasks in flight, 299 us with a warp per token and tensor), 32-bit ones, twice the bytes a task, with 64 registers (8191 tokens: 105 us; 153 us with 40).
 #include "msa_common.cuh"
 #include "msa_internal.h"
 
@@ -39,8 +39,8 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return
 // Threads of a CTA and CTAs an SM should hold, by element size and pairs per task.
 template <int V, typename TX>
 struct RopeCta {
-    static constexpr int kThreads = V < 8 ? 256 : sizeof(TX) == 2 ? 128 : 192;
-    static constexpr int kPerSm = V < 8 ? 2 : sizeof(TX) == 2 ? 12 : 5;
+    static constexpr int kThreads = V < 8 ? 256 : sizeof(TX) == 2 ? 96 : 192;
+    static constexpr int kPerSm = V < 8 ? 2 : sizeof(TX) == 2 ? 16 : 5;
     static constexpr int kTasks = V < 8 ? 4 : 1;  // per thread in flight
 };
 

@@ -92,11 +92,23 @@ __device__ __forceinline__ int tree_items(const TreeArgs& a, int b) {  // per gr
 __device__ __forceinline__ bool tree_unit(const TreeArgs& a, int unit, TreeUnit* u, int2* count) {
     const int lane = threadIdx.x & 31;
     const bool even = a.T <= (kRows >> a.lg_g);  // one item per sequence and group
+    // items per group of the sequences lo .. lo + n - 1, `per` of them a lane: a lane's, and up to and with the lane's
+    int lo = 0, n = a.B, per, mine, incl;
+    auto count_items = [&] {
+        per = (n + 31) / 32;
+        mine = 0;
+        for (int i = lane * per; i < min(n, (lane + 1) * per); ++i) mine += tree_items(a, lo + i);
+        incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += t;
+        }
+    };
     int live = a.B;
     if (!even) {
-        live = 0;
-        for (int b = lane; b < a.B; b += 32) live += tree_items(a, b);
-        live = __reduce_add_sync(0xffffffffu, live);
+        count_items();
+        live = __shfl_sync(0xffffffffu, incl, 31);
     }
     live *= a.H_kv;
     const int base = live < a.slots ? 0 : live / a.slots * a.slots, rem = live - base;
@@ -112,25 +124,18 @@ __device__ __forceinline__ bool tree_unit(const TreeArgs& a, int unit, TreeUnit*
         u->b = item / a.H_kv, u->r = item - u->b * a.H_kv, u->ct = 0;
         return true;
     }
-    int before = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int n = tree_items(a, b0 + lane), mine = n * a.H_kv;
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int t = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += t;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, before + incl > item);
-        if (past) {
-            const int l = __ffs(past) - 1;
-            const int at = item - before - __shfl_sync(0xffffffffu, incl - mine, l), per = __shfl_sync(0xffffffffu, n, l);
-            u->b = b0 + l, u->r = at / per, u->ct = at - u->r * per;
+    for (int before = 0;;) {  // to the lane that has the item, then among its sequences
+        const int l = __ffs(__ballot_sync(0xffffffffu, (before + incl) * a.H_kv > item)) - 1;
+        before += __shfl_sync(0xffffffffu, incl - mine, l);
+        lo += l * per;
+        if (per == 1) {
+            const int cts = __shfl_sync(0xffffffffu, mine, l), at = item - before * a.H_kv;
+            u->b = lo, u->r = at / cts, u->ct = at - u->r * cts;
             return true;
         }
-        before += __shfl_sync(0xffffffffu, incl, 31);
+        n = min(per, n - l * per);
+        count_items();
     }
-    return false;
 }
 
 // Zeros and LSE -inf for the rows of nodes n0 .. that lie in T.

@@ -427,3 +427,13 @@ def test_callers_workspace_and_output():
         c.attend(blocks, out=out, out_dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="parents"):
         msa.msa_tree_index_topk(c.dm, c.pages, msa.MsaTree(c.parents[:1], c.n_nodes), c.q_idx, c.k_idx, c.kip)
+
+
+def test_thousands_of_sequences_with_few_nodes():
+    """More sequences than a warp counts in one go: items found among 1100 sequences, most of them without a node."""
+    B, T = 1100, 9
+    nn = [T if b % 7 == 3 else 1 if b % 50 == 0 else 0 for b in range(B)]
+    c = Case([(b * 13) % 40 for b in range(B)], T, H_q=32, H_kv=1, d=64, di=32, bk=32, topk=1, n_nodes=nn, seed=23)
+    blocks = c.select()
+    out, lse = c.attend(blocks, want_lse=True)
+    c.check_attention(blocks, out, lse, nodes=[0, 8])
