@@ -437,3 +437,25 @@ def test_thousands_of_sequences_with_few_nodes():
     blocks = c.select()
     out, lse = c.attend(blocks, want_lse=True)
     c.check_attention(blocks, out, lse, nodes=[0, 8])
+
+
+def test_a_graph_replayed_with_other_trees():
+    """How the attention's work is spread depends on n_nodes on the device: a captured call follows it."""
+    g = torch.Generator().manual_seed(9)
+    B, T = 67, 20
+    lens = torch.randint(0, 400, (B,), generator=g).tolist()
+    c = Case(lens, T, H_q=32, H_kv=2, d=64, di=32, bk=32, topk=4, seed=24)
+    c.attend(c.select())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        blocks = c.select()
+        out, lse = c.attend(blocks, want_lse=True)
+    for nn in ([T] * B, [3] * B, [0] * B, [0] * (B - 1) + [T], torch.randint(0, T + 1, (B,), generator=g).tolist()):
+        c.n_nodes.copy_(torch.tensor(nn, dtype=I32))
+        graph.replay()
+        blocks2 = c.select()
+        out2, lse2 = c.attend(blocks2, want_lse=True)
+        torch.cuda.synchronize()
+        assert torch.equal(blocks, blocks2) and torch.equal(out, out2) and torch.equal(lse, lse2)
+    c.check_attention(blocks, out, lse, nodes=[0, 19])
