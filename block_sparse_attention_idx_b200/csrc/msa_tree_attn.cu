@@ -346,7 +346,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         if (id[x] < 0) continue;
         const int c = id[x], at = ls.before[c >> 5] + __popc(ls.bits[c >> 5] & ((1u << (c & 31)) - 1u));
         if (at < e_lo || at >= e_hi) continue;
-        atomicOr(&s.mask[at - e_lo], 1ull << list_of(tid + x * NT));
+        const int nl = list_of(tid + x * NT);
+        atomicOr(reinterpret_cast<uint32_t*>(&s.mask[at - e_lo]) + (nl >> 5), 1u << (nl & 31));
         s.page[at - e_lo] = pg[x];
     }
     // keys of the last page tile: the cache's last page, if chosen, holds len % block_k
