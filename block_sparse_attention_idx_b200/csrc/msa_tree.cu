@@ -28,7 +28,8 @@ namespace {
 // that the next sequence's load overlaps this one's tiles.
 // HBM-bound by design: each K_idx byte is read once for up to 256 rows. What else a tile costs is the issue of
 // one warp (waits, descriptors, commits): some 1000 cycles, as long as the 16 KB of a 128-token tile take to
-// arrive (1143 cycles a tile, 105 us for 16 x 262144 tokens); hence tiles of 256 tokens and warp-uniform loops.
+// arrive (1143 cycles a tile, 105 us for 16 sequences of up to 262144 tokens); hence tiles of 256 tokens and warp-uniform
+// loops: 71 us for the same 407 MB, 0.87 of the copy rate, what the loads alone take.
 constexpr int kScanThreads = 320;
 constexpr int kScanTile = 256;
 

@@ -24,7 +24,7 @@
 //
 // Bound, 64 nodes: the chain. A tile takes 3700 cycles, 2030 of them the exponentials and what is around them (1024 on
 // the MUFU, which both CTAs share), 1650 from P to the next S (1024 of products: 128 x 128 x 16 take 64 cycles with both
-// operands in shared memory); the tensor pipe is busy 32 % of the time, the MUFU 31 %. At 8 nodes a sequence (256 CTAs of
+// operands in shared memory); the tensor pipe is busy 38 % of the time, the MUFU 34 %. At 8 nodes a sequence (256 CTAs of
 // 6 tiles: 40 us with the merge) it waits for pages that nobody has read before (2300 cycles a tile for V), and list
 // building and output cost 9 us of a CTA's 28.
 #include <type_traits>
