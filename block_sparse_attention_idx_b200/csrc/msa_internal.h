@@ -239,6 +239,7 @@ struct TreeArgs {
     int32_t* blocks_out;             // [B, T, H_kv, topk+1]
     float* margin_out;               // [B, T, H_kv] or null
     const int32_t* blocks;
+    const __nv_bfloat16 *k, *v, *k_pool, *v_pool;  // set by run_tree_attn: the arrays behind its tensor maps
     int lg_g;                        // log2(H_q / H_kv)
     int k1_inv;                      // floor(2^16 / (topk + 1)) + 1: e / (topk + 1) = e * k1_inv >> 16 for e < 3800
     int slots;                       // attention CTAs that run at once

@@ -157,6 +157,61 @@ __device__ __forceinline__ void tree_zero_rows(const TreeArgs& a, int b, int r, 
     }
 }
 
+// One warp: half `hf` of the output columns of row `ri` of a CTA, by the definition, from the tokens that the row sees
+// among the drafted ones (if the CTA has them) and the entries [e_lo, e_hi) of the union. For rows whose product is not
+// finite: a weight of zero times an infinity or NaN in V (of a token that another node chose), or values so large that a
+// weight of up to 2^8 overflowed. lse2: the row's base-2 log-sum-exp over these tokens, so that no weight exceeds 1. A row
+// of 2176 tokens takes 0.3 ms, one warp's chain of loads; looking for such rows costs 2 us of the 140 at 64 nodes over
+// 16 x 65536 tokens.
+template <int D, int BK>
+__device__ __noinline__ void tree_row_by_tokens(const TreeArgs& a, const TreeAttnSmem<D>& s, const __nv_bfloat16* q, int b, int r, int n0,
+                                                int ri, int hf, bool drafted, int e_lo, int e_hi, int last_entry_keys, float lse2,
+                                                float* out, __nv_bfloat16* out_bf16) {
+    constexpr int KQ = D / 32, KV = D / 64, U = 4;  // elements of a key, of a value that a lane holds; tokens under way
+    const int lane = lane_id(), nl = ri >> a.lg_g;
+    const int64_t row = (((int64_t)b * a.T + n0 + nl) * a.H_q + (r << a.lg_g) + (ri & ((1 << a.lg_g) - 1)));
+    const float sl2 = a.scale * 1.4426950408889634f;
+    float qf[KQ], acc[KV];
+#pragma unroll
+    for (int x = 0; x < KQ; ++x) qf[x] = __bfloat162float(q[row * D + lane * KQ + x]);
+#pragma unroll
+    for (int x = 0; x < KV; ++x) acc[x] = 0.f;
+    auto tokens = [&](const __nv_bfloat16* k, const __nv_bfloat16* v, int64_t first, int n, unsigned long long which) {
+        for (int t0 = 0; t0 < n; t0 += U) {
+            float dot[U], vf[U][KV];
+#pragma unroll
+            for (int t = 0; t < U; ++t) {
+                const int64_t at = ((first + min(t0 + t, n - 1)) * a.H_kv + r) * D;
+                dot[t] = 0.f;
+#pragma unroll
+                for (int x = 0; x < KQ; ++x) dot[t] = fmaf(qf[x], __bfloat162float(k[at + lane * KQ + x]), dot[t]);
+#pragma unroll
+                for (int x = 0; x < KV; ++x) vf[t][x] = __bfloat162float(v[at + hf * (D / 2) + lane * KV + x]);
+            }
+#pragma unroll
+            for (int t = 0; t < U; ++t) {
+#pragma unroll
+                for (int o = 16; o; o >>= 1) dot[t] += __shfl_xor_sync(0xffffffffu, dot[t], o);
+                const float w = exp2f(fmaf(dot[t], sl2, -lse2));
+                if (t0 + t < n && ((which >> ((t0 + t) & 63)) & 1)) {
+#pragma unroll
+                    for (int x = 0; x < KV; ++x) acc[x] = fmaf(w, vf[t][x], acc[x]);
+                }
+            }
+        }
+    };
+    if (drafted) tokens(a.k, a.v, (int64_t)b * a.T, a.T, s.draft[nl]);
+    for (int e = e_lo; e < e_hi; ++e)
+        if ((s.mask[e - e_lo] >> nl) & 1)
+            tokens(a.k_pool, a.v_pool, (int64_t)s.page[e - e_lo] * BK, e == e_hi - 1 ? last_entry_keys : BK, ~0ull);
+#pragma unroll
+    for (int x = 0; x < KV; ++x) {
+        const int c = hf * (D / 2) + lane * KV + x;
+        if (out_bf16) out_bf16[c] = __float2bfloat16_rn(acc[x]);
+        else out[c] = acc[x];
+    }
+}
+
 template <int D, int BK>
 __global__ void __launch_bounds__(kAttnThreads, 2)
     k_tree_attn(const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
@@ -628,6 +683,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                 return ((int64_t)b * a.T + n0 + (i >> lg)) * a.H_q + (r << lg) + (i & ((1 << lg) - 1));
             };
             const bool write = hf == 0 && n0 + nl < a.T;
+            float odd_out = 0.f;  // NaN once one of the thread's outputs is not finite
             if (hf == 0 && part && row < a.part_rows) a.lse_part[u.part * a.part_rows + row] = lse;
             if (write && !part && a.lse) a.lse[out_row(row)] = lse;
             if (!part || n_tiles > 0) {
@@ -647,6 +703,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                         float f[32];
 #pragma unroll
                         for (int e = 0; e < 32; ++e) f[e] = has ? __uint_as_float(o[e]) * inv : 0.f;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) odd_out = fmaf(f[e], 0.f, odd_out);
 #pragma unroll
                         for (int e = 0; e < (kHalfOut ? 4 : 8); ++e) {
                             uint4 val;
@@ -673,6 +731,17 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                 if (part) store(std::false_type{}, a.o_part + (int64_t)u.part * a.part_rows * D, [](int i) { return i; });
                 else if (a.out_bf16) store(std::true_type{}, a.out_bf16, out_row);
                 else store(std::false_type{}, a.out, out_row);
+                // Rows with an output that is not finite, though no logit is NaN or +inf, again token by token.
+                __syncwarp();
+                for (unsigned again = __ballot_sync(0xffffffffu, odd_out != odd_out && l == l); again; again &= again - 1) {
+                    const int x = __ffs(again) - 1, ri = (warp & 3) * 32 + x;
+                    const float lse2 = __shfl_sync(0xffffffffu, mref + log2f(l), x);
+                    const int64_t to = (part ? (int64_t)u.part * a.part_rows + ri : out_row(ri)) * D;
+                    tree_row_by_tokens<D, BK>(a, s, q, b, r, n0, ri, hf, t0 == 0, e_lo, e_hi,
+                                              s.partial && e_hi == U ? len % BK : BK, lse2,
+                                              part ? a.o_part + to : a.out ? a.out + to : nullptr,
+                                              part || a.out ? nullptr : a.out_bf16 + to);
+                }
             }
         }
     }
@@ -700,7 +769,8 @@ __global__ void __launch_bounds__(256) k_tree_combine(const __grid_constant__ Tr
     float mx = my_l;
 #pragma unroll
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float my_w = my_l == -INFINITY ? 0.f : __expf(my_l - mx);
+    // (a part that saw a token keeps a weight above 0, so that a NaN or an infinity of its values is not lost)
+    const float my_e = __expf(my_l - mx), my_w = my_l == -INFINITY ? 0.f : my_e == 0.f ? __int_as_float(1) : my_e;
     float z = my_w;
 #pragma unroll
     for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
@@ -789,13 +859,16 @@ cudaError_t run_tree_attn(const TreeArgs& a, const void* q, const void* k, const
     const int items = tree_ctas(a.B, a.T, a.H_q, a.H_kv), parts = (int)tree_parts(a);
     const dim3 grid(items / a.slots * a.slots + (items % a.slots ? parts : 0));  // enough for any number of live items
     const auto* qb = static_cast<const __nv_bfloat16*>(q);
+    TreeArgs args = a;
+    args.k = static_cast<const __nv_bfloat16*>(k), args.v = static_cast<const __nv_bfloat16*>(v);
+    args.k_pool = static_cast<const __nv_bfloat16*>(k_pool), args.v_pool = static_cast<const __nv_bfloat16*>(v_pool);
     auto pick = [&](auto d_c, auto bk_c) -> cudaError_t {
         constexpr int D = decltype(d_c)::value, BK = decltype(bk_c)::value;
         const size_t smem = std::max<size_t>(sizeof(TreeAttnSmem<D>) + 1024, 100 * 1024);  // at most two CTAs an SM
         auto kern = k_tree_attn<D, BK>;
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        kern<<<grid, kAttnThreads, smem, st>>>(kp, vp, kd, vd, a, qb);
+        kern<<<grid, kAttnThreads, smem, st>>>(kp, vp, kd, vd, args, qb);
         return cudaGetLastError();
     };
     using I32 = std::integral_constant<int, 32>;
