@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                     m0 = max3n(m0, m1, max3n(f[30], f[31], f[31]));
                     const bool strange = !(m0 < INFINITY);
                     odd = odd || strange;
-                    // a NaN or infinite score that the row sees makes the row NaN
+                    // a NaN or +inf score that the row sees makes the row NaN (-inf is a weight of zero)
                     if (strange && see[c]) l2 = r2 = f2_packf(NAN, NAN);
                     mx = see[c] ? fmaxf(mx, m0) : mx;
                 }

@@ -434,9 +434,10 @@ MSA_API msa_status msa_tree_index_topk(const msa_dims *dims, const msa_pages *pa
  *   lse    fp32 [B, T, H_q] or NULL: natural-log sum-exp of the scaled logits                     (output)
  * A row that sees no token has output 0 and LSE -inf. An infinity or NaN in V reaches the rows that see its token, in
  * its column, and only those (the rows that share a product with it are evaluated token by token, which is slow: 20 ms
- * for 64 nodes over 16 x 65536 tokens if every row has to be). A NaN or infinite logit makes the rows that see it NaN, and
- * only those. What lies behind the last token, in pages or in
- * the drafted arrays, may be anything.
+ * for 64 nodes over 16 x 65536 tokens if every row has to be).
+ * A logit of NaN or +inf makes the rows that see it NaN, and only those; one of -inf is a weight of zero, and a row of
+ * only such logits has output 0 and LSE -inf. What lies behind the last token, in pages or in the drafted arrays, may be
+ * anything.
  */
 MSA_API msa_status msa_tree_sparse_attn(const msa_dims *dims, const msa_pages *pages, const msa_tree *tree,
                                         const void *q, const void *k, const void *v, const void *k_pool,

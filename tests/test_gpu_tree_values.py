@@ -147,3 +147,33 @@ def test_a_bad_value_in_a_captured_call():
     page.copy_(keep)
     graph.replay()
     assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS, ids=["bk32", "bk128", "bk64"])
+def test_logits_of_minus_infinity_are_weights_of_zero(layout):
+    """Block 2's keys are -inf in one element: by the sign of its query a row of node 0 has logits of -inf, which count
+    for nothing, or +inf, which make it NaN. With block 2 alone nothing is left: output 0 and LSE -inf, as with no token."""
+    c, lists = _case(layout)
+    c.kp[int(c.table[0, 2]), :, :, 7] = -INF
+    out, lse = c.attend(lists, want_lse=True)
+    without = lists.clone()
+    without[:, 0, :, 2] = -1
+    _, l2 = c.attend(without, want_lse=True)
+    plus = c.q[0, 0, :, 7] < 0
+    assert plus.any() and not plus.all() and not (c.q[0, 0, :, 7] == 0).any()
+    assert torch.isnan(out[0, 0, plus]).all() and torch.isnan(lse[0, 0, plus]).all()
+    # the others as over the lists without block 2 (their sums may be cut elsewhere: equal to the bounds, not in bits)
+    ids, keep = without.cpu().numpy(), torch.ones(4, c.dm.H_q, dtype=torch.bool, device=DEV)
+    keep[0] = ~plus
+    for n in range(4):
+        o, dev, mag = _node(c, ids, 0, n)
+        tol = 2 * (2.0 ** -8 / (1 - 2.0 ** -8) + 3e-5) * dev + 4e-5 * mag
+        ok = np.abs(out[0, n].double().cpu().numpy() - o) <= tol
+        assert ok[keep[n].cpu().numpy()].all()
+    assert (lse[0] - l2[0])[keep].abs().max() <= 6e-5
+    alone = torch.full_like(lists, -1)
+    alone[:, 0, :, 0] = 2
+    for dtype in (torch.float32, torch.bfloat16):
+        out, lse = c.attend(alone, want_lse=True, out_dtype=dtype)
+        assert (out[0, 0, ~plus] == 0).all() and torch.isneginf(lse[0, 0, ~plus]).all()
+        assert torch.isnan(out[0, 0, plus]).all() and (out[0, 1:] == 0).all() and torch.isneginf(lse[0, 1:]).all()
