@@ -1,0 +1,59 @@
+"""Selection for trees: the Top-k variant that ranks a row's 513 to 2048 blocks with one warp, which takes 16 rows an SM, and
+what a sequence's selection and attention keep when the batch around it changes."""
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_attention_idx_b200 as msa
+from oracle import tree as otree
+from test_gpu_tree import Case
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def _rows():
+    return 16 * torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("bk,topk,L", [(32, 16, 20000), (64, 16, 131071), (128, 5, 90000), (32, 1, 65536)])
+def test_many_rows_of_up_to_2048_blocks(bk, topk, L):
+    """Rows enough to fill the device: a warp a row, up to 64 candidates a lane."""
+    T, H_kv = 64, 8
+    B = -(-_rows() // (T * H_kv))
+    assert 512 < -(-L // 256) * (256 // bk) <= 2048
+    lens = [L - 37 * b for b in range(B)]
+    c = Case(lens, T, H_q=H_kv, H_kv=H_kv, d=64, di=32, bk=bk, topk=topk, seed=81, N=L, n_nodes=[T] * (B - 1) + [T - 3])
+    blocks, margin = c.select(want_margin=True)
+    c.check_selection(blocks, margin, nodes=[0, T - 4, T - 1])
+
+
+@pytest.mark.parametrize("lanes", [1, 15, 17])
+def test_the_largest_maxima_in_few_lanes(lanes):
+    """Lane l of the warp holds the maxima of blocks 4 l + {0 .. 3} + 128 j. With all large ones in `lanes` lanes, those
+    lanes' candidates all pass the bound when there are no more than topk of them: up to 16 x 64 of the list's room."""
+    T, H_kv, bk, topk, L = 64, 8, 32, 16, 2040 * 32
+    B = -(-_rows() // (T * H_kv))
+    c = Case([L] * B, T, H_q=H_kv, H_kv=H_kv, d=64, di=32, bk=bk, topk=topk, seed=82, N=L, kind="roots")
+    blk = torch.arange(L // bk, device=DEV)
+    high = (blk // 4) % 32 < lanes
+    for b in range(B):  # the first element of a key decides, the queries all take it
+        k = c.kip[c.table[b, :L // bk].long()]
+        k[:, :, 0] = torch.where(high, 4.0, -4.0)[:, None].to(k.dtype)
+        c.kip[c.table[b, :L // bk].long()] = k
+    c.q_idx[..., 0] = 4.0
+    c.q_idx[..., 1:] /= 16  # (2^-8 steps, times keys in 2^-4 steps: still exact)
+    blocks, margin = c.select(want_margin=True)
+    c.check_selection(blocks, margin, nodes=[0, 31, 63])
+    assert high[blocks[..., :topk].long()].all()
+
+
+def test_fewer_lanes_with_blocks_than_chosen_ones():
+    """Short sequences in a long table: the variant is chosen by the table, most lanes hold no block."""
+    T, H_kv, bk = 64, 8, 32
+    B = max(-(-_rows() // (T * H_kv)), 7)
+    lens = [0, 1, 31, 5 * 32, 64 * 32 - 1, 64 * 32, 128 * 32 + 7] + [3000] * (B - 7)
+    c = Case(lens, T, H_q=H_kv, H_kv=H_kv, d=64, di=32, bk=bk, topk=16, seed=83, N=2048 * 32)
+    blocks, margin = c.select(want_margin=True)
+    c.check_selection(blocks, margin, nodes=[0, 63])
