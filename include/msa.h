@@ -29,7 +29,7 @@
  *   kernel skips the offending work, sets a flag in the status word and returns; read it with
  *   msa_get_device_status.
  * - Deterministic: the same inputs give bit-identical `blocks`, attention outputs, LSEs and KL
- *   loss. dK_idx and the attention gradients are accumulated with float32 atomics and may differ
+ *   loss (on the same device: msa_tree_sparse_attn says what else its last bits go by). dK_idx and the attention gradients are accumulated with float32 atomics and may differ
  *   in the last bits.
  *
  * Supported sizes (MSA_ERR_UNSUPPORTED otherwise): d in {64, 128}, d_idx in {32, 64},
@@ -432,6 +432,9 @@ MSA_API msa_status msa_tree_index_topk(const msa_dims *dims, const msa_pages *pa
  *          normally msa_tree_index_topk's output. Without the local block the node does not see itself.
  *   out    fp32 [B, T, H_q, d], or bf16 (the same result, rounded to nearest even) for the _bf16 entry (output)
  *   lse    fp32 [B, T, H_q] or NULL: natural-log sum-exp of the scaled logits                     (output)
+ * How a sequence's keys are split over CTAs goes by n_nodes of the whole batch and the device's SM count: the same
+ * sequence in another batch has the same selection bit for bit, and the same output and LSE up to the roundings of
+ * that split (of the weights to bf16, 2^-8 each, and of the merge in fp32).
  * A row that sees no token has output 0 and LSE -inf. An infinity or NaN in V reaches the rows that see its token, in
  * its column, and only those (the rows that share a product with it are evaluated token by token, which is slow: 20 ms
  * for 64 nodes over 16 x 65536 tokens if every row has to be).

@@ -57,3 +57,43 @@ def test_fewer_lanes_with_blocks_than_chosen_ones():
     c = Case(lens, T, H_q=H_kv, H_kv=H_kv, d=64, di=32, bk=bk, topk=16, seed=83, N=2048 * 32)
     blocks, margin = c.select(want_margin=True)
     c.check_selection(blocks, margin, nodes=[0, 63])
+
+
+def _sub(c, keep):
+    """The sequences `keep` of a case, over the same pools."""
+    x = object.__new__(Case)
+    x.__dict__.update(c.__dict__)
+    at = torch.tensor(keep, device=DEV)
+    x.dm = msa.MsaDims(len(keep), *[getattr(c.dm, f) for f in ("N", "H_q", "H_kv", "d", "d_idx", "block_k", "topk")])
+    for f in ("table", "lens", "parents", "n_nodes", "q", "q_idx", "k", "v", "k_idx"):
+        setattr(x, f, getattr(c, f)[at].contiguous())
+    x.pages, x.tree = msa.MsaPages(x.table, x.lens), msa.MsaTree(x.parents, x.n_nodes)
+    return x
+
+
+@pytest.mark.parametrize("T,H_q,H_kv,d,bk", [(12, 64, 4, 128, 128), (40, 32, 1, 64, 32)])
+def test_a_sequence_alone_and_in_other_batches(T, H_q, H_kv, d, bk):
+    """Selection and margins do not depend on the batch, bit for bit. The attention's split of a sequence's keys does, by the
+    other sequences' node counts: two results lie within twice the bound of one, 2 (2^-8 / (1 - 2^-8) + 3e-5) dev +
+    4e-5 mag, where dev <= 2 mag."""
+    lens = [1500, 300, 77, 4000, 0, 900]
+    c = Case(lens, T, H_q=H_q, H_kv=H_kv, d=d, di=64, bk=bk, topk=16, seed=8, n_nodes=[T, T - 1, T, 1, T, 0])
+    g = torch.Generator(device=DEV).manual_seed(85)
+    for x in (c.q_idx, c.k_idx, c.kip):  # off the grid: sums that depend on their order
+        x.copy_(torch.where(torch.isnan(x), x, torch.randn(x.shape, generator=g, device=DEV).to(x.dtype)))
+    blocks, margin = c.select(want_margin=True)
+    out, lse = c.attend(blocks, want_lse=True)
+    for keep in ([0], [1], [2], [3], [4], [5], [3, 0], [5, 2, 1, 4], [1] * 7 + [0]):
+        s = _sub(c, keep)
+        b2, m2 = s.select(want_margin=True)
+        assert torch.equal(b2, blocks[keep]) and torch.equal(m2, margin[keep])
+        o2, l2 = s.attend(b2, want_lse=True)
+        for i, b in enumerate(keep):
+            nn = int(c.n_nodes[b])
+            assert torch.equal(o2[i, nn:], out[b, nn:]) and torch.equal(l2[i, nn:], lse[b, nn:])
+            for n in sorted({0, nn // 2, nn - 1}) if nn else []:
+                K, V, _ = c.virtual(b, n)
+                _, _, mag = otree.attend(c.od, c.q[b, n].cpu(), K, V, blocks[b, n].cpu().numpy())
+                tol = 2 * (4 * (2.0 ** -8 / (1 - 2.0 ** -8) + 3e-5) + 4e-5) * mag
+                assert (np.abs((o2[i, n] - out[b, n]).cpu().numpy()) <= tol).all()
+            assert (l2[i, :nn] - lse[b, :nn]).abs().nan_to_num(0.0).max() <= 6e-5 if nn else True
