@@ -3,9 +3,10 @@
 //   y_a = amp (x_a cos - x_b sin),  y_b = amp (x_a sin + x_b cos),  (a, b) = (i, i + rot/2) or (2i, 2i+1).
 // The gradient applies the transposed map: the same with -sin.
 //
-// Angles. position * inv_freq reaches 1e6 radians, where 32 bits leave 0.06 radians of error. The angle is formed
-// in turns in 64 bits, t = position * (inv_freq / 2 pi), the whole turns are dropped and sincospif takes
-// 2 (t - rint t) in [-1, 1]: about four 64-bit operations and one sincospif a pair, once per token and distinct
+// Angles. position * inv_freq reaches 1e6 radians and more, where 32 bits leave 0.06 radians of error, and 2^31, where a
+// product in 64 bits leaves 2e-7. The angle is formed in turns, t = position * (inv_freq / 2 pi), both products as a sum of
+// two 64-bit numbers (the rounding of a product is a fused multiply-add away), the whole turns are dropped and sincospif
+// takes 2 (t - rint t) in about [-1, 1]: some ten 64-bit operations and one sincospif a pair, once per token and distinct
 // table of frequencies (Q and K share one, Q_idx and K_idx another).
 //
 // HBM-bound: every element is read and written once. A CTA takes one token's heads of all tensors as a flat list of
@@ -44,6 +45,15 @@ struct RopeCta {
     static constexpr int kTasks = V < 8 ? 4 : 1;  // per thread in flight
 };
 
+// 2 t, t = pos * f / (2 pi) less its whole turns. Up to |pos * f| < 2^48 the low parts stay below 1/32 of a turn, and the
+// result is that of the exact angle rounded to fp32.
+__device__ __forceinline__ float rope_half_turns(double pos, double f) {
+    constexpr double kTurn = 0.15915494309189535, kTurnLow = -9.839338337591243e-18;  // 1 / (2 pi)
+    const double w = f * kTurn, w_low = fma(f, kTurn, -w) + f * kTurnLow;
+    const double t = pos * w, t_low = fma(pos, w, -t) + pos * w_low;
+    return (float)(2.0 * ((t - rint(t)) + t_low));
+}
+
 // gridDim.y CTAs share a token's tasks where the tokens alone are too few.
 template <int V, bool IL, typename TX, typename TY>
 __global__ void __launch_bounds__(RopeCta<V, TX>::kThreads, RopeCta<V, TX>::kPerSm) k_rope(const __grid_constant__ RopeArgs a) {
@@ -81,9 +91,8 @@ __global__ void __launch_bounds__(RopeCta<V, TX>::kThreads, RopeCta<V, TX>::kPer
                 int tab = 0;
                 while (i >= a.tab0[tab + 1]) ++tab;
                 const RopeSeg& g = a.seg[a.tab_seg[tab]];
-                const double t = pos * (g.inv_freq[i - a.tab0[tab]] * 0.15915494309189535);  // turns: 1 / (2 pi)
                 float sn, cn;
-                sincospif((float)(2.0 * (t - rint(t))), &sn, &cn);
+                sincospif(rope_half_turns(pos, g.inv_freq[i - a.tab0[tab]]), &sn, &cn);
                 s_cos[tab * kMaxPairs + i - a.tab0[tab]] = cn * g.amp;
                 s_sin[tab * kMaxPairs + i - a.tab0[tab]] = sn * (a.back ? -g.amp : g.amp);
             }

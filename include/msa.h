@@ -323,8 +323,9 @@ MSA_API msa_status msa_kl_dense_fwd_grad(const msa_dims *dims, const void *q, co
  * with (a, b) = (i, i + rot/2), or (2i, 2i+1) with `interleaved`. msa_rope_fwd applies it, msa_rope_bwd its
  * transpose (-sin in place of sin): the gradient dx of an upstream dy (passed as x, written to y), and for
  * amp = 1 the inverse rotation. One call rotates up to 8 tensors (Q, K, Q_idx and K_idx of a step) in one
- * launch. Angles are reduced to a fraction of a turn in 64 bits, so that far positions keep their accuracy;
- * cos and sin are fp32 (absolute error below 3e-7), the rotation is fp32, rounded once to y's type.
+ * launch. Angles are reduced to a fraction of a turn in twice 64 bits, so that every position keeps its accuracy;
+ * cos and sin are fp32 (absolute error below 3e-7 for |position * inv_freq| < 2^48, which every position and a
+ * frequency below 2^17 meet), the rotation is fp32, rounded once to y's type.
  *   seg        host array of nseg tensors (read during the call), 1 <= nseg <= 8
  *     x, y       [tokens, heads, dim] of x_type / y_type; the heads x dim elements of a token contiguous,
  *                tokens x_stride / y_stride elements apart (a multiple of 16 bytes, at least heads * dim).
