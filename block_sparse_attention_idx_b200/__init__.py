@@ -368,7 +368,8 @@ def msa_rope_inv_freq(rot: int, base: float = 10000.0, scaling: str | None = Non
       "linear"  positions divided by factor (every frequency / factor)
       "ntk"     base * factor ** (rot / (rot - 2)): the lowest frequency is divided by factor, the highest kept
       "yarn"    frequencies that turn at least 32 times over orig_len tokens are kept, those that turn at most
-                once are divided by factor, a linear ramp over i between; amp = 0.1 ln(factor) + 1
+                once are divided by factor, a linear ramp over i between (from pair 0 where none turns 32 times);
+                amp = 0.1 ln(factor) + 1
     """
     if rot < 2 or rot % 2:
         raise ValueError(f"rot must be even and at least 2, got {rot}")
@@ -391,6 +392,8 @@ def msa_rope_inv_freq(rot: int, base: float = 10000.0, scaling: str | None = Non
 
         lo, hi = max(math.floor(pair(32)), 0), min(math.ceil(pair(1)), rot - 1)
         ramp = ((torch.arange(rot // 2, dtype=torch.float64) - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        if orig_len <= 2 * math.pi:  # not even pair 0 turns more than once
+            ramp = torch.ones_like(ramp)
         f = f / factor * ramp + f * (1 - ramp)
         amp = 0.1 * math.log(factor) + 1
     return f.to(device) if device is not None else f, amp
