@@ -589,7 +589,10 @@ def tree_workspace(op: int, dims: MsaDims, T: int, device) -> torch.Tensor:
 
 @functools.lru_cache(maxsize=256)
 def _tree_ws_size(op, B, N, H_q, H_kv, d, d_idx, block_k, topk, T, device) -> int:
-    """msa_tree_workspace_size for sizes seen before on a device (it depends on the device's SM count)."""
+    """msa_tree_workspace_size for sizes seen before on a device (it depends on the SM count of the current one)."""
+    if device != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{device}, but the current CUDA device is cuda:{torch.cuda.current_device()}; "
+                         "call under torch.cuda.device(...)")
     return max(256, msa_tree_workspace_size(op, MsaDims(B, N, H_q, H_kv, d, d_idx, block_k, topk), T))
 
 
