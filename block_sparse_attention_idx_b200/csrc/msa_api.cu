@@ -3,6 +3,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "msa.h"
@@ -237,6 +238,8 @@ msa_status rope_call(const msa_rope_seg* seg, int nseg, int64_t tokens, const in
         if (g.x_stride < row || g.y_stride < row || g.x_stride >= (1LL << 40) || g.y_stride >= (1LL << 40) ||
             g.x_stride * xs % 16 != 0 || g.y_stride * ys % 16 != 0)
             return MSA_ERR_INVALID_ARG;
+        // (no memory spans 2^60 bytes; below, the ends that overlap() compares fit 64 bits)
+        if ((double)tokens * std::max(g.x_stride * xs, g.y_stride * ys) >= 1152921504606846976.0) return MSA_ERR_INVALID_ARG;
         xr[i] = {reinterpret_cast<uintptr_t>(g.x), tokens, row * xs, g.x_stride * xs};
         yr[i] = {reinterpret_cast<uintptr_t>(g.y), tokens, row * ys, g.y_stride * ys};
         if (overlap(xr[i], yr[i]) && (g.x != g.y || g.x_stride != g.y_stride || xs != ys)) return MSA_ERR_INVALID_ARG;
