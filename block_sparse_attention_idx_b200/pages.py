@@ -155,9 +155,14 @@ class PagedCache:
     def append(self, seqs, k, v, k_idx, counts=None, rows=None, stream=None) -> None:
         """Writes counts[i] new tokens (default: all T) behind sequence seqs[i]: the first rows of k, v
         [B,T,H_kv,d], k_idx [B,T,d_idx], or rows[i] (lists of row numbers, e.g. an accepted path of tree nodes, whose
-        lengths are then the counts). Reserves what is needed first."""
-        seqs = list(seqs)
-        T = k.shape[1]
+        lengths are then the counts). Reserves what is needed first; arguments that do not fit are refused before that."""
+        seqs, d = list(seqs), self.dims
+        T = k.shape[1] if k.dim() == 4 else 0
+        shape = (len(seqs), T, d.H_kv, d.d)
+        for t, name, want in ((k, "k", shape), (v, "v", shape), (k_idx, "k_idx", (len(seqs), T, d.d_idx))):
+            if tuple(t.shape) != want or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != self.k_pool.device:
+                raise ValueError(f"{name}: expected contiguous torch.bfloat16 {want} on {self.k_pool.device}, got {t.dtype} "
+                                 f"{tuple(t.shape)} on {t.device}")
         if rows is not None:
             rows = [[int(x) for x in r] for r in rows]
             if counts is not None and [int(c) for c in counts] != [len(r) for r in rows]:
@@ -166,8 +171,8 @@ class PagedCache:
                 raise ValueError(f"row numbers must be in [0, {T})")
             counts = [len(r) for r in rows]
         counts = [T] * len(seqs) if counts is None else [int(c) for c in counts]
-        if len(counts) != len(seqs) or k.shape[0] != len(seqs):
-            raise ValueError(f"{len(seqs)} sequences, {len(counts)} counts, {k.shape[0]} rows of new tokens")
+        if len(counts) != len(seqs):
+            raise ValueError(f"{len(seqs)} sequences, {len(counts)} counts")
         if rows is None and any(c > T for c in counts):
             raise ValueError(f"counts must be at most {T}")
         self.reserve(seqs, counts, stream=stream)
