@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                             m0 = max3f(m0, f[e], f[e + 1]);
                             m1 = max3f(m1, f[e + 2], f[e + 3]);
                         }
-                        cmax[hf * 2 + q] = max3f(m0, m1, fmaxf(f[30], f[31]));
+                        cmax[hf * 2 + q] = fmaxf(max3f(m0, m1, fmaxf(f[30], f[31])), -INFINITY);  // all NaN: -inf
                     }
                 }
                 if (row < R) {
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kTopkWarps * 32) k_tree_topk(const __grid_cons
                         dot = fmaf(qf.y, kf.y, dot);
                     }
                 }
-                atomicMax(&s_draft[slot][c - full], (uint32_t)(cand_key(dot, 0) >> 32));
+                atomicMax(&s_draft[slot][c - full], (uint32_t)(cand_key(fmaxf(dot, -INFINITY), 0) >> 32));  // NaN: -inf
             }
             __syncwarp();
             for (int c = full + lane; c < local; c += 32) {

@@ -421,6 +421,7 @@ MSA_API msa_status msa_tree_workspace_size(int op, const msa_dims *dims, int T, 
  *   q_idx bf16 [B, T, H_kv, d_idx]; k_idx bf16 [B, T, d_idx] (drafted); k_idx_pool the cache's
  *   blocks int32 [B, T, H_kv, topk+1]                                                         (output)
  *   margin_out fp32 [B, T, H_kv] or NULL: the cutoff margin of msa_sparse_attn_decode         (output)
+ * A score of NaN does not count, as in msa_sparse_attn_decode: a block of no other scores ranks with maximum -inf.
  */
 MSA_API msa_status msa_tree_index_topk(const msa_dims *dims, const msa_pages *pages, const msa_tree *tree,
                                        const void *q_idx, const void *k_idx, const void *k_idx_pool, int32_t *blocks,

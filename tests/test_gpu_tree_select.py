@@ -11,6 +11,7 @@ from test_gpu_tree import Case
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
+NAN = float("nan")
 
 
 def _rows():
@@ -97,3 +98,38 @@ def test_a_sequence_alone_and_in_other_batches(T, H_q, H_kv, d, bk):
                 tol = 2 * (4 * (2.0 ** -8 / (1 - 2.0 ** -8) + 3e-5) + 4e-5) * mag
                 assert (np.abs((o2[i, n] - out[b, n]).cpu().numpy()) <= tol).all()
             assert (l2[i, :nn] - lse[b, :nn]).abs().nan_to_num(0.0).max() <= 6e-5 if nn else True
+
+
+@pytest.mark.parametrize("layout", [dict(H_q=8, H_kv=2, d=64, di=32, bk=32, topk=4), dict(H_q=16, H_kv=4, d=128, di=64, bk=128, topk=3),
+                                    dict(H_q=4, H_kv=4, d=64, di=64, bk=64, topk=4)], ids=["bk32", "bk128", "bk64"])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_that_are_nan_do_not_count(layout, sign):
+    """As in the oracle and the decode step: NaN keys in a block leave its other keys' maximum, a block of NaN keys has the
+    maximum -inf, and so has everything for a NaN query; cached and drafted keys alike."""
+    bk = layout["bk"]
+    # a chain over a cache that ends two tokens before a block's end: node 1 fills it, node 2 opens the next
+    c = Case([10 * bk - 2], 5, kind="chain", seed=87, **layout)
+    c.q_idx[..., :4] = 4.0
+    for x in (c.kip, c.k_idx):  # all scores around 64, or around -64
+        x[..., :4] = torch.where(torch.isnan(x[..., :4]), x[..., :4], torch.full_like(x[..., :4], 4.0 * sign))
+    c.kip[int(c.table[0, 2])] = NAN
+    c.kip[int(c.table[0, 5]), :-1] = NAN
+    c.kip[int(c.table[0, 5]), -1] = c.q_idx[0, 3, 0]  # what is left leads for node 3
+    c.kip[int(c.table[0, 9]), :bk - 2] = NAN              # of the last block the drafted tokens' alone are numbers
+    c.q_idx[0, 4, 0] = NAN
+    for bad in (None, 0, 1):  # no, one and both of the drafted tokens that share the cache's last block
+        if bad is not None:
+            c.k_idx[0, bad] = NAN
+        blocks = c.select().cpu().numpy()
+        for n in range(5):
+            K, V, KI = c.virtual(0, n)
+            want, _, _, _ = otree.node_decode(c.od, c.q[0, n].cpu(), c.q_idx[0, n].cpu(), K, V, KI)
+            assert (blocks[0, n] == want).all(), (bad, n, blocks[0, n], want)
+    assert 5 in blocks[0, 3, 0] and 2 not in blocks[0, 3, 0]
+    dm = msa.MsaDims(1, c.dm.N + 1, *[getattr(c.dm, f) for f in ("H_q", "H_kv", "d", "d_idx", "block_k", "topk")])
+    dense = [torch.zeros(1, c.dm.N + 1, *p.shape[2:], dtype=torch.bfloat16, device=DEV) for p in (c.kp, c.vp, c.kip)]
+    for n in range(5):  # the framework's decode step on the path
+        for t, x in zip(dense, c.virtual(0, n)):
+            t[0, :x.shape[0]] = x
+        step = msa.msa_sparse_attn_decode(dm, c.lens + n + 1, c.q[0, n][None], c.q_idx[0, n][None], *dense)[1]
+        assert (step[0].cpu().numpy() == blocks[0, n]).all(), n
