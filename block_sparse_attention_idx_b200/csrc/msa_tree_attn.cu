@@ -769,24 +769,24 @@ __global__ void __launch_bounds__(256) k_tree_combine(const __grid_constant__ Tr
     float mx = my_l;
 #pragma unroll
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    // (a part that saw a token keeps a weight above 0, so that a NaN or an infinity of its values is not lost)
-    const float my_e = __expf(my_l - mx), my_w = my_l == -INFINITY ? 0.f : my_e == 0.f ? __int_as_float(1) : my_e;
-    float z = my_w;
+    // Of a part that saw no token the weight is -1 here: its output may never have been written, and is dropped. That of
+    // one whose weight underflows to 0 is not: an infinity or NaN there makes the row NaN, as it does within a part.
+    const float my_w = my_l == -INFINITY ? -1.f : __expf(my_l - mx);
+    float z = my_l == -INFINITY ? 0.f : my_w;
 #pragma unroll
     for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     constexpr int kPer = D / 32;
     float acc[kPer];
 #pragma unroll
     for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
-    // Six parts under way at a time, without branches (one by one the 18 parts of a single node took 4 us longer). A part
-    // of weight 0 may never have been written: what it holds is dropped.
+    // Six parts under way at a time, without branches (one by one the 18 parts of a single node took 4 us longer).
     for (int p0 = 0; p0 < splits; p0 += 6) {
         float f[6][kPer], wp[6];
 #pragma unroll
         for (int i = 0; i < 6; ++i) {
             const int p = min(p0 + i, splits - 1);
             wp[i] = __shfl_sync(0xffffffffu, my_w, p);
-            if (p0 + i >= splits) wp[i] = 0.f;
+            if (p0 + i >= splits) wp[i] = -1.f;
             const float* o = a.o_part + (int64_t)(first + p * step) * D + lane * kPer;
             if (kPer == 4) {
                 const float4 v = *reinterpret_cast<const float4*>(o);
@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(256) k_tree_combine(const __grid_constant__ Tr
 #pragma unroll
         for (int i = 0; i < 6; ++i)
 #pragma unroll
-            for (int x = 0; x < kPer; ++x) acc[x] = fmaf(wp[i], wp[i] == 0.f ? 0.f : f[i][x], acc[x]);
+            for (int x = 0; x < kPer; ++x) acc[x] = wp[i] < 0.f ? acc[x] : fmaf(wp[i], f[i][x], acc[x]);
     }
     const float inv = z > 0.f || z != z ? 1.f / z : 0.f;
     if (a.out_bf16) {

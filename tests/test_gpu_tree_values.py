@@ -177,3 +177,20 @@ def test_logits_of_minus_infinity_are_weights_of_zero(layout):
         out, lse = c.attend(alone, want_lse=True, out_dtype=dtype)
         assert (out[0, 0, ~plus] == 0).all() and torch.isneginf(lse[0, 0, ~plus]).all()
         assert torch.isnan(out[0, 0, plus]).all() and (out[0, 1:] == 0).all() and torch.isneginf(lse[0, 1:]).all()
+
+
+def test_a_value_that_is_not_finite_counts_however_small_its_weight():
+    """Block 0 weighs e^-1000 and holds a NaN and an infinity: by the definition's 0 times either, NaN in their columns for
+    the rows that see it. In one CTA, and where the block has a CTA of its own and the merge joins them."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for B in (1, sms + 1):
+        c, lists = _case(LAYOUTS[1], B=B, T=2, seed=76)
+        lists[:, 1, :, 0] = -1  # node 1 does not see block 0
+        c.q[..., 0] = 8.0
+        c.kp[c.table[:, 0].long(), :, :, 0] = -2048.0  # logits of about -1448 against others of order 10
+        c.vp[c.table[:, 0].long(), 3, :, 5] = NAN
+        c.vp[c.table[:, 0].long(), 4, :, 6] = INF
+        out, lse = c.attend(lists, want_lse=True)
+        bad = torch.isnan(out).all(0).all(1)
+        assert torch.isnan(out[:, 0, :, 5:7]).all() and torch.isfinite(out[:, 1]).all() and torch.isfinite(lse).all()
+        assert bad[0, 5] and bad[0, 6] and int((~torch.isfinite(out)).sum()) == 2 * B * c.dm.H_q
