@@ -57,8 +57,8 @@ struct TreeLists {
 
 template <int D>
 struct TreeAttnSmem {
-    alignas(1024) uint8_t q[kRows * D * 2];  // with k, at the end: outputs on their way out
-    alignas(1024) uint8_t k[kTile * D * 2];
+    alignas(1024) uint8_t q[kRows * D * 2];
+    alignas(1024) uint8_t k[kTile * D * 2];  // with v, at the end: outputs on their way out
     alignas(1024) uint8_t v[kTile * D * 2];
     unsigned long long mask[kMaxEntries];  // nodes of the CTA that chose the entry
     unsigned long long draft[64];          // drafted tokens that a node attends
@@ -164,16 +164,18 @@ __device__ __forceinline__ void tree_zero_rows(const TreeArgs& a, int b, int r, 
 // of 2176 tokens takes 0.3 ms, one warp's chain of loads; looking for such rows costs 2 us of the 140 at 64 nodes over
 // 16 x 65536 tokens.
 template <int D, int BK>
-__device__ __noinline__ void tree_row_by_tokens(const TreeArgs& a, const TreeAttnSmem<D>& s, const __nv_bfloat16* q, int b, int r, int n0,
-                                                int ri, int hf, bool drafted, int e_lo, int e_hi, int last_entry_keys, float lse2,
-                                                float* out, __nv_bfloat16* out_bf16) {
+__device__ __noinline__ void tree_row_by_tokens(const TreeArgs& a, const TreeAttnSmem<D>& s, int b, int r, int ri, int hf, bool drafted,
+                                                int e_lo, int e_hi, int last_entry_keys, float lse2, float* out,
+                                                __nv_bfloat16* out_bf16) {
     constexpr int KQ = D / 32, KV = D / 64, U = 4;  // elements of a key, of a value that a lane holds; tokens under way
     const int lane = lane_id(), nl = ri >> a.lg_g;
-    const int64_t row = (((int64_t)b * a.T + n0 + nl) * a.H_q + (r << a.lg_g) + (ri & ((1 << a.lg_g) - 1)));
     const float sl2 = a.scale * 1.4426950408889634f;
     float qf[KQ], acc[KV];
 #pragma unroll
-    for (int x = 0; x < KQ; ++x) qf[x] = __bfloat162float(q[row * D + lane * KQ + x]);
+    for (int x = 0; x < KQ; ++x) {
+        const int c = lane * KQ + x;
+        qf[x] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(s.q + (c / 64) * (kTile * 128) + swz(ri, (c % 64) * 2, 128)));
+    }
 #pragma unroll
     for (int x = 0; x < KV; ++x) acc[x] = 0.f;
     auto tokens = [&](const __nv_bfloat16* k, const __nv_bfloat16* v, int64_t first, int n, unsigned long long which) {
@@ -658,8 +660,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             if (lane == 0) mbar_arrive(&s.p_ready);
         }
         // -------------------------------------------------------------------- outputs
-        // Through shared memory (Q and K are no longer read: the last S was issued before the last PV), so that a warp
-        // writes whole rows: 32 rows of 16-byte pieces straight from the lanes took 4 us at the end of every CTA.
+        // Through shared memory (K and V are no longer read: the last PV is done), so that a warp writes whole rows: 32 rows
+        // of 16-byte pieces straight from the lanes took 4 us at the end of every CTA. Q stays, for rows that are evaluated
+        // token by token (the output may be written over the queries).
         if (ok && n_tiles > 0) {
             bool done = false;
             for (int i = 0; i < 32 && !done; ++i) done = mbar_try_wait(&s.pv_done, 0);  // before the timed wait's loads
@@ -687,7 +690,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             if (hf == 0 && part && row < a.part_rows) a.lse_part[u.part * a.part_rows + row] = lse;
             if (write && !part && a.lse) a.lse[out_row(row)] = lse;
             if (!part || n_tiles > 0) {
-                uint8_t* stage = s.q + warp * (32 * CW * 4);
+                uint8_t* stage = s.k + warp * (32 * CW * 4);
                 auto store = [&](auto half_c, auto* base, auto at) {  // row i goes to row at(i) of base
                     constexpr bool kHalfOut = decltype(half_c)::value;
                     constexpr int LP = (kHalfOut ? 1 : 2) + (CW == 64 ? 2 : 1), P = 1 << LP;  // 16-byte pieces of a row
@@ -737,7 +740,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                     const int x = __ffs(again) - 1, ri = (warp & 3) * 32 + x;
                     const float lse2 = __shfl_sync(0xffffffffu, mref + log2f(l), x);
                     const int64_t to = (part ? (int64_t)u.part * a.part_rows + ri : out_row(ri)) * D;
-                    tree_row_by_tokens<D, BK>(a, s, q, b, r, n0, ri, hf, t0 == 0, e_lo, e_hi,
+                    tree_row_by_tokens<D, BK>(a, s, b, r, ri, hf, t0 == 0, e_lo, e_hi,
                                               s.partial && e_hi == U ? len % BK : BK, lse2,
                                               part ? a.o_part + to : a.out ? a.out + to : nullptr,
                                               part || a.out ? nullptr : a.out_bf16 + to);

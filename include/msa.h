@@ -433,6 +433,7 @@ MSA_API msa_status msa_tree_index_topk(const msa_dims *dims, const msa_pages *pa
  *   blocks int32 [B, T, H_kv, topk+1]: ids in [0, b_n], -1 entries ignored, an id given twice counts once;
  *          normally msa_tree_index_topk's output. Without the local block the node does not see itself.
  *   out    fp32 [B, T, H_q, d], or bf16 (the same result, rounded to nearest even) for the _bf16 entry (output)
+ *          the latter may be q itself
  *   lse    fp32 [B, T, H_q] or NULL: natural-log sum-exp of the scaled logits                     (output)
  * How a sequence's keys are split over CTAs goes by n_nodes of the whole batch and the device's SM count: the same
  * sequence in another batch has the same selection bit for bit, and the same output and LSE up to the roundings of

@@ -194,3 +194,15 @@ def test_a_value_that_is_not_finite_counts_however_small_its_weight():
         bad = torch.isnan(out).all(0).all(1)
         assert torch.isnan(out[:, 0, :, 5:7]).all() and torch.isfinite(out[:, 1]).all() and torch.isfinite(lse).all()
         assert bad[0, 5] and bad[0, 6] and int((~torch.isfinite(out)).sum()) == 2 * B * c.dm.H_q
+
+
+@pytest.mark.parametrize("layout", LAYOUTS, ids=["bk32", "bk128", "bk64"])
+@pytest.mark.parametrize("B", [1, 150])
+def test_the_output_in_place_of_the_queries(layout, B):
+    """bf16 outputs written over q, rows that are evaluated token by token among them."""
+    c, lists = _case(layout, B=B, seed=77)
+    c.vp[c.table[:, 3].long(), 5, 0, 3] = NAN
+    c.vp[c.table[:, 4].long(), 6, :, 9] = INF
+    want, wlse = c.attend(lists, want_lse=True, out_dtype=torch.bfloat16)
+    got, lse = c.attend(lists, want_lse=True, out_dtype=torch.bfloat16, out=c.q)
+    assert got is c.q and torch.equal(got.view(torch.int16), want.view(torch.int16)) and torch.equal(lse, wlse)
