@@ -23,13 +23,14 @@
 // have one buffer each: K of the next tile arrives during this tile's exponentials, V during the next tile's. The last
 // wave of CTAs, if it would fill at most half of the device, splits its unions over several CTAs, merged by
 // k_tree_combine: 64 nodes over 16 x 65536 tokens (408 items of 128 rows, 30 tiles each; 64 query heads in 4 groups,
-// d = 128) take 132 us instead of 144, and a few nodes of a long tree take what they would take alone.
+// d = 128) took 132 us instead of 144 by that, and a few nodes of a long tree take what they would take alone.
 //
-// Bound, 64 nodes: the chain. A tile takes 3700 cycles, 2030 of them the exponentials and what is around them (1024 on
-// the MUFU, which both CTAs share), 1650 from P to the next S (1024 of products: 128 x 128 x 16 take 64 cycles with both
-// operands in shared memory); the tensor pipe is busy 38 % of the time, the MUFU 34 %. At 8 nodes a sequence (256 CTAs of
-// 6 tiles: 40 us with the merge) it waits for pages that nobody has read before (2300 cycles a tile for V), and list
-// building and output cost 9 us of a CTA's 28.
+// Bound, 64 nodes (140 us, 1.09 TB/s and 380 TFLOP/s): the chain. Before the rounded weights had their own sum (134 us)
+// a tile took 3700 cycles, 2030 of them the exponentials and what is around them (1024 on the MUFU, which both CTAs share),
+// 1650 from P to the next S (1024 of products: 128 x 128 x 16 take 64 cycles with both operands in shared memory); the
+// tensor pipe is busy 39 % of the time, the MUFU 32 %. At 8 nodes a sequence (256 CTAs of 6 tiles: 39 us with the merge) it
+// waits for pages that nobody has read before (2300 cycles a tile for V), and list building and output cost 9 us of a CTA's
+// 28.
 #include <type_traits>
 
 #include "msa_tree.cuh"

@@ -438,6 +438,9 @@ MSA_API msa_status msa_tree_index_topk(const msa_dims *dims, const msa_pages *pa
  * How a sequence's keys are split over CTAs goes by n_nodes of the whole batch and the device's SM count: the same
  * sequence in another batch has the same selection bit for bit, and the same output and LSE up to the roundings of
  * that split (of the weights to bf16, 2^-8 each, and of the merge in fp32).
+ * Accuracy: logits, sums and the LSE are fp32. The weights w_j enter the product with V rounded to bf16, 2^-8 of each at
+ * most, and are normalised as rounded: the output is off by at most 2^-8 / (1 - 2^-8) of sum_j w_j |v_j - out| (twice that
+ * where a sequence's keys are split over CTAs), besides fp32 roundings. msa_sparse_attn_decode does the same.
  * A row that sees no token has output 0 and LSE -inf. An infinity or NaN in V reaches the rows that see its token, in
  * its column, and only those (the rows that share a product with it are evaluated token by token, which is slow: 20 ms
  * for 64 nodes over 16 x 65536 tokens if every row has to be).
